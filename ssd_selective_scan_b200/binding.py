@@ -1,4 +1,5 @@
-"""ctypes binding of libssd.so -- the C ABI declared in include/ssd.h.
+"""ctypes binding of libssd.so -- the C ABI declared in include/ssd.h and
+include/ssd_diag.h.
 
 Argument marshalling only: every function here passes integers (device
 pointers, sizes, a cudaStream_t handle) straight to the C entry point of the
@@ -59,6 +60,20 @@ SIGNATURES = {
                            _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.c_float, _i, _vp, _sz, _vp, _vp]),
 }
 
+# The entry points of include/ssd_diag.h.
+DIAG_SIGNATURES = {
+    "ssd_state_map_workspace_bytes": (_sz, [_i]),
+    "ssd_state_map": (_i, [_vp] * 5 + [_i] * 6 + [_vp] * 8 + [_sz, _vp, _vp]),
+    "ssd_conv1d_silu_varlen": (_i, [_vp, _i64, _vp, _i64] + [_vp] * 7 + [_i] * 7 + [_vp, _vp]),
+    "ssd_conv1d_silu_bwd_workspace_bytes": (_sz, [_i] * 4),
+    "ssd_conv1d_silu_bwd": (_i, [_vp] * 9 + [_i] * 5 + [_vp, _sz, _vp]),
+    "ssd_diag_scan_workspace_bytes": (_sz, [_i] * 5),
+    "ssd_diag_scan_fwd": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 6 + [_i] * 6 + [_vp, _sz, _vp]),
+    "ssd_diag_scan_fwd_varlen": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 9 + [_i] * 8 +
+                                 [_vp, _sz, _vp, _vp]),
+    "ssd_diag_state_update": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 8 + [_i] * 8 + [_vp, _vp]),
+}
+
 _lock = threading.Lock()
 _lib = None
 
@@ -79,7 +94,7 @@ def load() -> ctypes.CDLL:
                     f"libssd.so not found at {LIB_PATH}: build it with "
                     "`python -m ssd_selective_scan_b200.build` (there is no fallback path)")
             lib = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in SIGNATURES.items():
+            for name, (res, args) in (SIGNATURES | DIAG_SIGNATURES).items():
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
@@ -197,3 +212,57 @@ def ssd_mixer_fwd(hidden, W_in, conv_w, conv_bias, conv_state, dt_bias, A, D, no
     return load().ssd_mixer_fwd(hidden, W_in, conv_w, conv_bias, conv_state, dt_bias, A, D, norm_w, W_out,
                                 init_state, out, final_state, b, L, d_model, H, P, N, G, Q, k, norm_groups, eps,
                                 dtype, workspace, workspace_bytes, status, stream)
+
+
+def ssd_state_map_workspace_bytes(n) -> int:
+    return load().ssd_state_map_workspace_bytes(n)
+
+
+def ssd_state_map(lens, ctx, table, free_list, free_head, n, max_blocks, nfree, T, block_tokens, nslots, cu_seqlens,
+                  seq_of, pos_of, slot_of, init_slot, table_out, free_head_out, workspace, workspace_bytes, status,
+                  stream) -> int:
+    return load().ssd_state_map(lens, ctx, table, free_list, free_head, n, max_blocks, nfree, T, block_tokens, nslots,
+                                cu_seqlens, seq_of, pos_of, slot_of, init_slot, table_out, free_head_out, workspace,
+                                workspace_bytes, status, stream)
+
+
+def ssd_conv1d_silu_varlen(x, x_stride, out, out_stride, w, bias, cache, cu_seqlens, seq_of, slot_of, init_slot, nseq, T,
+                           E, k, block_tokens, nslots, dtype, status, stream) -> int:
+    return load().ssd_conv1d_silu_varlen(x, x_stride, out, out_stride, w, bias, cache, cu_seqlens, seq_of, slot_of,
+                                         init_slot, nseq, T, E, k, block_tokens, nslots, dtype, status, stream)
+
+
+def ssd_conv1d_silu_bwd_workspace_bytes(b, L, E, k) -> int:
+    return load().ssd_conv1d_silu_bwd_workspace_bytes(b, L, E, k)
+
+
+def ssd_conv1d_silu_bwd(x, w, bias, conv_state, dout, dx, dw, dbias, dconv_state, b, L, E, k, dtype, workspace,
+                        workspace_bytes, stream) -> int:
+    return load().ssd_conv1d_silu_bwd(x, w, bias, conv_state, dout, dx, dw, dbias, dconv_state, b, L, E, k, dtype,
+                                      workspace, workspace_bytes, stream)
+
+
+def ssd_diag_scan_workspace_bytes(nseq, rows, E, N, G) -> int:
+    return load().ssd_diag_scan_workspace_bytes(nseq, rows, E, N, G)
+
+
+def ssd_diag_scan_fwd(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D, init_state, y,
+                      final_state, b, L, E, N, G, dtype, workspace, workspace_bytes, stream) -> int:
+    return load().ssd_diag_scan_fwd(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D,
+                                    init_state, y, final_state, b, L, E, N, G, dtype, workspace, workspace_bytes, stream)
+
+
+def ssd_diag_scan_fwd_varlen(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D, states, y,
+                             cu_seqlens, seq_of, slot_of, init_slot, nseq, T, E, N, G, block_tokens, nslots, dtype,
+                             workspace, workspace_bytes, status, stream) -> int:
+    return load().ssd_diag_scan_fwd_varlen(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D,
+                                           states, y, cu_seqlens, seq_of, slot_of, init_slot, nseq, T, E, N, G,
+                                           block_tokens, nslots, dtype, workspace, workspace_bytes, status, stream)
+
+
+def ssd_diag_state_update(states, u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D, y,
+                          cu_seqlens, seq_of, slot_of, init_slot, nseq, rows, E, N, G, block_tokens, nslots, dtype, status,
+                          stream) -> int:
+    return load().ssd_diag_state_update(states, u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias,
+                                        D, y, cu_seqlens, seq_of, slot_of, init_slot, nseq, rows, E, N, G, block_tokens,
+                                        nslots, dtype, status, stream)

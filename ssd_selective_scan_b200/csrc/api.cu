@@ -5,6 +5,7 @@
 
 #include <cuda_bf16.h>
 
+#include "abi.h"
 #include "kernels.h"
 #include "decode.h"
 #include "scan_bwd.h"
@@ -13,40 +14,15 @@ namespace {
 
 using ssd::ScanArgs;
 
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-};
-
-Range span(const void* p, int64_t bytes)
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + (uintptr_t)(bytes > 0 ? bytes : 0)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-bool valid_dtype(ssd_dtype_t d) { return d == SSD_F32 || d == SSD_BF16; }
-
-int elem_bytes(ssd_dtype_t d) { return d == SSD_F32 ? 4 : 2; }
-
-ssd_status_t from_cuda(cudaError_t e)
-{
-    if (e == cudaSuccess) return SSD_OK;
-    (void)cudaGetLastError();
-    return SSD_ERR_CUDA;
-}
-
-int max_optin_smem()
-{
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return 0;
-    return v;
-}
-
-size_t round_up_256(size_t n) { return (n + 255) / 256 * 256; }
+using ssd::aligned;
+using ssd::elem_bytes;
+using ssd::from_cuda;
+using ssd::max_optin_smem;
+using ssd::overlap;
+using ssd::Range;
+using ssd::round_up_256;
+using ssd::span;
+using ssd::valid_dtype;
 
 }  // namespace
 

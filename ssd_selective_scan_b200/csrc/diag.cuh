@@ -1,0 +1,182 @@
+// diag.cuh -- device helpers of the diagonal selective scan's kernels.
+#pragma once
+
+#include "common.cuh"
+#include "ssd.h"
+
+namespace ssd {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Packed fp32 pairs: one instruction, each half rounded as the scalar one.
+__device__ inline float2 pk_fma(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ inline float2 pk_mul(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// 2^v on the special-function unit (2 ulp; results below 2^-126 become 0).
+__device__ inline float ex2(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in [0, 1], with
+// log1p(e) = 2 atanh(w), w = e / (2 + e) <= 1/3, by the series
+// 2 w (1 + w^2/3 + ... + w^12/13): the first term left out is below 2e-8 of
+// the sum, so the result is good to a few ulp at every v (an e of zero gives
+// max(v, 0); NaN stays NaN).
+__device__ inline float softplus_series(float v)
+{
+    const float e = expf(-fabsf(v));
+    const float w = __fdividef(e, 2.0f + e);
+    const float q = w * w;
+    float p = fmaf(q, 1.0f / 13.0f, 1.0f / 11.0f);
+    p = fmaf(q, p, 1.0f / 9.0f);
+    p = fmaf(q, p, 1.0f / 7.0f);
+    p = fmaf(q, p, 1.0f / 5.0f);
+    p = fmaf(q, p, 1.0f / 3.0f);
+    p = fmaf(q, p, 1.0f);
+    return fmaxf(v, 0.0f) + (w + w) * p;
+}
+
+// 1 / (1 + e^-v)
+__device__ inline float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+// d SiLU(v) / dv, given sigmoid(v)
+__device__ inline float dsilu_f(float v, float sg) { return sg * fmaf(v, 1.0f - sg, 1.0f); }
+
+// 8 adjacent elements as they lie in memory: 16 bytes (bf16) or 32 (f32).
+template <typename T> struct Raw8 {
+    uint4 q[sizeof(T) / 2];
+    __device__ inline void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ inline void load(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ inline float get(int j) const { return io<T>::word_get(reinterpret_cast<const uint32_t*>(q), j); }
+    __device__ static inline void store(T* p, const float (&v)[8])
+    {
+        if constexpr (sizeof(T) == 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+};
+
+// A packed batch's requests and state slots (device pointers; see ssd_diag.h).
+struct Slots {
+    const int32_t* cu;         // [nseq + 1]
+    const int32_t* seq_of;     // [T]
+    const int64_t* slot_of;    // [T]
+    const int32_t* init_slot;  // [nseq]
+    int nseq, nslots, block;
+    int32_t* status;
+};
+
+__device__ inline void flag_invalid(int32_t* status)
+{
+    if (status) atomicExch(reinterpret_cast<int*>(status), (int)SSD_ERR_INVALID_ARG);
+}
+
+// The slot that token t's block lives in, or -1 (and the status word set) if
+// the map names none.
+__device__ inline int slot_at(const Slots& s, int64_t flat)
+{
+    if (flat < 0 || flat >= (int64_t)s.nslots * s.block) {
+        flag_invalid(s.status);
+        return -1;
+    }
+    return (int)(flat / s.block);
+}
+
+// One piece of one sequence: the tokens t0 .. t1-1 of the rows, in sequence
+// r = [s0, s1).  Pieces are cut at the multiples of `seg` along the packed
+// rows, so that each is found from its index alone: index q < nseq is
+// sequence q's first piece, index nseq + m - 1 the piece that starts at row
+// m * seg where that row lies inside a sequence.  A row nearer than `keep` to
+// its sequence's start begins no piece (the first piece runs on over it).
+struct Piece {
+    int r, t0, t1, s0, s1;
+};
+
+template <bool PACKED>
+__device__ inline bool find_piece(int q, const Slots& sl, int nseq, int L, int rows, int seg, int keep, Piece& p)
+{
+    auto bounds = [&](int r) {
+        if constexpr (PACKED) {
+            p.s0 = sl.cu[r];
+            p.s1 = sl.cu[r + 1];
+            if (p.s0 < 0 || p.s1 < p.s0 || p.s1 > rows) {
+                flag_invalid(sl.status);
+                return false;
+            }
+        } else {
+            p.s0 = r * L;
+            p.s1 = p.s0 + L;
+        }
+        p.r = r;
+        return true;
+    };
+    if (q < nseq) {
+        if (!bounds(q) || p.s1 == p.s0) return false;
+        p.t0 = p.s0;
+    } else {
+        const int64_t at = (int64_t)(q - nseq + 1) * seg;
+        if (at >= rows) return false;
+        int r;
+        if constexpr (PACKED) {
+            r = sl.seq_of[at];
+            if (r < 0) return false;       // behind the last sequence
+            if (r >= nseq) {
+                flag_invalid(sl.status);
+                return false;
+            }
+        } else {
+            r = (int)(at / L);
+        }
+        if (!bounds(r)) return false;
+        if (at < p.s0 || at >= p.s1) {
+            flag_invalid(sl.status);
+            return false;
+        }
+        if (at - p.s0 <= keep) return false;
+        p.t0 = (int)at;
+    }
+    int64_t cut = ((int64_t)p.t0 / seg + 1) * seg;
+    if (p.t0 == p.s0 && cut - p.s0 <= keep) cut += seg;
+    p.t1 = (int)(cut < p.s1 ? cut : p.s1);
+    return true;
+}
+
+}  // namespace ssd

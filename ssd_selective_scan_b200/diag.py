@@ -1,0 +1,348 @@
+"""Torch-facing calls of the diagonal selective scan (include/ssd_diag.h): the
+state map of a batch of requests, the packed short conv and the conv's
+gradient, the scan (dense, packed, backward) and the single-token update.
+
+As in ``layer``, each function checks its tensors, allocates what it was not
+given, passes raw pointers to the C entry point of the same name and raises
+``SsdError`` on any non-OK status.  Work runs on the current stream of the
+tensors' device, or on ``stream``.
+
+A serving step with these calls::
+
+    m = state_map(lens, ctx, table, free_list, free_head, T, block_tokens, nslots, status=status)
+    u = conv1d_silu_varlen(x, conv_w, conv_cache, m, bias=conv_bias, status=status)
+    dt_raw, B, C = projections of u
+    y = diag_scan_fwd_varlen(u, dt_raw, A, B, C, states, m, dt_bias=dt_bias, D=D, z=z, status=status)
+
+(``diag_state_update`` in the last line's place where every request brings one
+token); ``status`` is read by the caller after synchronising, and 0 means that
+every check on the device passed.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import binding as libssd
+from .layer import _dtype_code, _ptr
+
+
+class StateMap(NamedTuple):
+    """Where a packed batch's requests, rows and states are (device tensors;
+    the layouts are ssd_diag.h's).  The packed calls read cu_seqlens, seq_of,
+    slot_of and init_slot; table and free_head are the scheduler's for the
+    next step."""
+    cu_seqlens: torch.Tensor          # [n + 1] int32
+    seq_of: torch.Tensor              # [T] int32
+    pos_of: torch.Tensor | None       # [T] int32
+    slot_of: torch.Tensor             # [T] int64
+    init_slot: torch.Tensor           # [n] int32
+    table: torch.Tensor | None        # [n, max_blocks] int32
+    free_head: torch.Tensor | None    # [1] int32
+    block_tokens: int
+
+
+class _On:
+    """The device and stream of a call: the tensors' device is made current
+    for it, and what the call allocates is tied to `stream` where that is not
+    the current one."""
+
+    def __init__(self, like: torch.Tensor, stream):
+        if not like.is_cuda:
+            raise ValueError("CUDA tensors expected")
+        self.device = like.device
+        self.given = stream
+        self.switch = None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.switch = torch.cuda.device(self.device)
+            self.switch.__enter__()
+        s = torch.cuda.current_stream() if self.given is None else self.given
+        if self.given is not None and s.device != self.device:
+            if self.switch is not None:
+                self.switch.__exit__(None, None, None)
+            raise ValueError("stream and tensors are on different devices")
+        self.other = self.given is not None and s != torch.cuda.current_stream()
+        self.stream = s
+        self.handle = s.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.switch is not None:
+            self.switch.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other:
+            t.record_stream(self.stream)
+        return t
+
+    def workspace(self, given, need: int):
+        """(pointer, bytes) of the caller's workspace, or of a new one."""
+        if given is None:
+            if not need:
+                return None, 0
+            given = self.empty(need, torch.uint8)
+            self.kept = given
+        _on_device(given, "workspace", self.device)
+        if not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return given.data_ptr(), given.numel() * given.element_size()
+
+
+def _on_device(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _dense(t, name, dtype, shape, device):
+    """A contiguous tensor of this type and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, name, lead, E, like) -> tuple[int | None, int]:
+    """(pointer, row stride) of a [*lead, E] tensor whose rows are evenly
+    spaced and dense."""
+    if t is None:
+        return None, E
+    if tuple(t.shape) != (*lead, E) or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {(*lead, E)} on {like.device}")
+    st = t.stride()
+    rows = 1
+    for k in lead:
+        rows *= k
+    if rows == 0:
+        return None, E
+    if st[-1] != 1 or (len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]):
+        raise ValueError(f"{name} must have dense, evenly spaced rows")
+    # a dimension of one row says nothing about the spacing
+    rs = st[-2] if lead[-1] > 1 else (st[0] if len(lead) == 2 and lead[0] > 1 else E)
+    return t.data_ptr(), rs
+
+
+def _bc(B, C, lead, like) -> tuple[int | None, int | None, int, int, int]:
+    """B, C [*lead, G, N] as (pointer, pointer, row stride, G, N)."""
+    if B.dim() != len(lead) + 2 or B.shape != C.shape:
+        raise ValueError("B and C must share the shape [.., G, N]")
+    G, N = B.shape[-2], B.shape[-1]
+    out = []
+    for t, name in ((B, "B"), (C, "C")):
+        if N > 1 and t.stride(-1) != 1 or G > 1 and t.stride(-2) != N:
+            raise ValueError(f"{name}: dense (G, N) rows expected")
+        out.append(_rows(t.flatten(-2) if t.numel() else t.reshape(*lead, G * N), name, lead, G * N, like))
+    (pB, sB), (pC, sC) = out
+    if sB != sC:
+        raise ValueError("B and C must share one row stride")
+    return pB, pC, sB, G, N
+
+
+def _map(m: StateMap, T: int, device):
+    """The pointers of a StateMap, its requests and block size."""
+    n = m.cu_seqlens.numel() - 1
+    return (_dense(m.cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), device), _dense(m.seq_of, "seq_of", torch.int32, (T,), device),
+            _dense(m.slot_of, "slot_of", torch.int64, (T,), device), _dense(m.init_slot, "init_slot", torch.int32, (n,), device), n)
+
+
+def _status(status, on):
+    if status is None:
+        status = on.empty(1, torch.int32)
+        with torch.cuda.stream(on.stream):
+            status.zero_()
+        on.kept_status = status
+    return _dense(status, "status", torch.int32, (1,), on.device)
+
+
+def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_list: torch.Tensor, free_head: torch.Tensor,
+              T: int, block_tokens: int, nslots: int, *, out: StateMap | None = None, workspace: torch.Tensor | None = None,
+              status: torch.Tensor | None = None, stream=None) -> StateMap:
+    """The map of a batch of requests: lens, ctx [n] int32 (new and held
+    tokens), table [n, max_blocks] int32 (slots of the held blocks), free_list
+    [nfree] and free_head [1] int32; T rows in the packed batch.  Returns a
+    StateMap whose table and free_head are the updated ones (new tensors, or
+    `out`'s, which may be the inputs for an update in place).  A batch that
+    does not fit (ssd_diag.h) leaves SSD_ERR_INVALID_ARG in `status` and gives
+    an empty map."""
+    n = lens.numel()
+    i32 = torch.int32
+    if table.dim() != 2 or table.shape[0] != n:
+        raise ValueError("table must be [n, max_blocks]")
+    mb = table.shape[1]
+    if out is not None and out.block_tokens != block_tokens:
+        raise ValueError("out was made for another block size")
+    with _On(lens, stream) as on:
+        dev = on.device
+        if out is None:
+            out = StateMap(on.empty(n + 1, i32), on.empty(T, i32), on.empty(T, i32), on.empty(T, torch.int64), on.empty(n, i32),
+                           on.empty((n, mb), i32), on.empty(1, i32), block_tokens)
+        cu, seq, slot, init, _ = _map(out, T, dev)
+        pos = _dense(out.pos_of, "pos_of", i32, (T,), dev)
+        wp, wb = on.workspace(workspace, int(libssd.ssd_state_map_workspace_bytes(n)))
+        st = libssd.ssd_state_map(
+            _dense(lens, "lens", i32, (n,), dev), _dense(ctx, "ctx", i32, (n,), dev), _dense(table, "table", i32, (n, mb), dev),
+            _dense(free_list, "free_list", i32, (free_list.numel(),), dev), _dense(free_head, "free_head", i32, (1,), dev),
+            n, mb, free_list.numel(), T, block_tokens, nslots, cu, seq, pos, slot, init,
+            _dense(out.table, "out.table", i32, (n, mb), dev), _dense(out.free_head, "out.free_head", i32, (1,), dev), wp, wb,
+            _status(status, on), on.handle)
+        libssd.check("ssd_state_map", st)
+    return out
+
+
+def conv1d_silu_varlen(x: torch.Tensor, w: torch.Tensor, cache: torch.Tensor, m: StateMap, *, bias: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal depthwise conv1d + SiLU over packed requests.  x [T, E] (dense
+    rows at any stride); w [E, k] f32; cache [nslots, E, k] of x's dtype,
+    read and written by slot.  Returns out [T, E]; rows behind the last
+    request are left as they were."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, E]")
+    T, E = x.shape
+    k = w.shape[-1]
+    with _On(x, stream) as on:
+        dev = on.device
+        if out is None:
+            out = on.empty((T, E), x.dtype)
+        xp, xs = _rows(x, "x", (T,), E, x)
+        op, os_ = _rows(out, "out", (T,), E, x)
+        cu, seq, slot, init, n = _map(m, T, dev)
+        nslots = cache.shape[0]
+        st = libssd.ssd_conv1d_silu_varlen(xp, xs, op, os_, _dense(w, "w", torch.float32, (E, k), dev),
+                                           _dense(bias, "bias", torch.float32, (E,), dev),
+                                           _dense(cache, "cache", x.dtype, (nslots, E, k), dev), cu, seq, slot, init, n, T, E, k,
+                                           m.block_tokens, nslots, _dtype_code(x), _status(status, on), on.handle)
+        libssd.check("ssd_conv1d_silu_varlen", st)
+    return out
+
+
+def conv1d_silu_bwd(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, bias: torch.Tensor | None = None,
+                    conv_state: torch.Tensor | None = None, *, workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients through conv1d_silu.  x, dout [b, L, E]; w [E, k] f32, bias
+    [E] f32, conv_state [b, E, k] (the cache as the forward call found it).
+    Returns dict(dx, dw, dbias, dconv_state): dx and dconv_state in the I/O
+    dtype, dw and dbias f32; None for what the forward call did not have."""
+    if x.dim() != 3:
+        raise ValueError("x must be [b, L, E]")
+    b, L, E = x.shape
+    k = w.shape[-1]
+    f32 = torch.float32
+    with _On(x, stream) as on:
+        dev = on.device
+        r = dict(dx=on.empty((b, L, E), x.dtype), dw=on.empty((E, k), f32), dbias=None if bias is None else on.empty(E, f32),
+                 dconv_state=None if conv_state is None else on.empty((b, E, k), x.dtype))
+        wp, wb = on.workspace(workspace, int(libssd.ssd_conv1d_silu_bwd_workspace_bytes(b, L, E, k)))
+        st = libssd.ssd_conv1d_silu_bwd(_dense(x, "x", x.dtype, (b, L, E), dev), _dense(w, "w", f32, (E, k), dev),
+                                        _dense(bias, "bias", f32, (E,), dev), _dense(conv_state, "conv_state", x.dtype, (b, E, k), dev),
+                                        _dense(dout, "dout", x.dtype, (b, L, E), dev), _ptr(r["dx"]), _ptr(r["dw"]), _ptr(r["dbias"]),
+                                        _ptr(r["dconv_state"]), b, L, E, k, _dtype_code(x), wp, wb, on.handle)
+        libssd.check("ssd_conv1d_silu_bwd", st)
+    return r
+
+
+def diag_scan_workspace_bytes(nseq: int, rows: int, E: int, N: int, G: int) -> int:
+    """Workspace of diag_scan_fwd (nseq = b, rows = b * L) and of
+    diag_scan_fwd_varlen (rows = T)."""
+    return int(libssd.ssd_diag_scan_workspace_bytes(nseq, rows, E, N, G))
+
+
+def diag_scan_fwd(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *,
+                  dt_bias: torch.Tensor | None = None, D: torch.Tensor | None = None, z: torch.Tensor | None = None,
+                  init_state: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                  final_state: torch.Tensor | bool | None = True, workspace: torch.Tensor | None = None, stream=None):
+    """The diagonal scan of a dense batch.  u, dt_raw, z [b, L, E], B, C
+    [b, L, G, N] (views with dense rows at any stride), A [E, N] f32, dt_bias,
+    D [E] f32, init_state [b, E, N] f32.  Returns (y [b, L, E], final_state
+    [b, E, N] f32 or None)."""
+    if u.dim() != 3:
+        raise ValueError("u must be [b, L, E]")
+    b, L, E = u.shape
+    f32 = torch.float32
+    with _On(u, stream) as on:
+        dev = on.device
+        pB, pC, bcs, G, N = _bc(B, C, (b, L), u)
+        if y is None:
+            y = on.empty((b, L, E), u.dtype)
+        if final_state is True:
+            final_state = on.empty((b, E, N), f32)
+        elif final_state is False:
+            final_state = None
+        up, us = _rows(u, "u", (b, L), E, u)
+        dp, ds = _rows(dt_raw, "dt_raw", (b, L), E, u)
+        zp, zs = _rows(z, "z", (b, L), E, u)
+        wp, wb = on.workspace(workspace, int(libssd.ssd_diag_scan_workspace_bytes(b, b * L, E, N, G)))
+        st = libssd.ssd_diag_scan_fwd(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
+                                      _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
+                                      _dense(init_state, "init_state", f32, (b, E, N), dev), _dense(y, "y", u.dtype, (b, L, E), dev),
+                                      _dense(final_state, "final_state", f32, (b, E, N), dev), b, L, E, N, G, _dtype_code(u), wp, wb,
+                                      on.handle)
+        libssd.check("ssd_diag_scan_fwd", st)
+    return y, final_state
+
+
+def diag_scan_fwd_varlen(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                         states: torch.Tensor, m: StateMap, *, dt_bias: torch.Tensor | None = None, D: torch.Tensor | None = None,
+                         z: torch.Tensor | None = None, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The diagonal scan of packed requests.  u, dt_raw, z [T, E], B, C
+    [T, G, N]; states [nslots, E, N] f32, read and written by slot.  Returns y
+    [T, E]; rows behind the last request are left as they were."""
+    if u.dim() != 2:
+        raise ValueError("u must be [T, E]")
+    T, E = u.shape
+    f32 = torch.float32
+    with _On(u, stream) as on:
+        dev = on.device
+        pB, pC, bcs, G, N = _bc(B, C, (T,), u)
+        if y is None:
+            y = on.empty((T, E), u.dtype)
+        up, us = _rows(u, "u", (T,), E, u)
+        dp, ds = _rows(dt_raw, "dt_raw", (T,), E, u)
+        zp, zs = _rows(z, "z", (T,), E, u)
+        cu, seq, slot, init, n = _map(m, T, dev)
+        nslots = states.shape[0]
+        wp, wb = on.workspace(workspace, int(libssd.ssd_diag_scan_workspace_bytes(n, T, E, N, G)))
+        st = libssd.ssd_diag_scan_fwd_varlen(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
+                                             _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
+                                             _dense(states, "states", f32, (nslots, E, N), dev), _dense(y, "y", u.dtype, (T, E), dev),
+                                             cu, seq, slot, init, n, T, E, N, G, m.block_tokens, nslots, _dtype_code(u), wp, wb,
+                                             _status(status, on), on.handle)
+        libssd.check("ssd_diag_scan_fwd_varlen", st)
+    return y
+
+
+def diag_state_update(states: torch.Tensor, u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                      C: torch.Tensor, m: StateMap | None = None, *, dt_bias: torch.Tensor | None = None,
+                      D: torch.Tensor | None = None, z: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One token per request, states [nslots, E, N] f32 updated in place by
+    slot (without a map row i is state i).  u, dt_raw, z [rows, E], B, C
+    [rows, G, N].  Returns y [rows, E]."""
+    if u.dim() != 2:
+        raise ValueError("u must be [rows, E]")
+    T, E = u.shape
+    f32 = torch.float32
+    with _On(u, stream) as on:
+        dev = on.device
+        pB, pC, bcs, G, N = _bc(B, C, (T,), u)
+        if y is None:
+            y = on.empty((T, E), u.dtype)
+        up, us = _rows(u, "u", (T,), E, u)
+        dp, ds = _rows(dt_raw, "dt_raw", (T,), E, u)
+        zp, zs = _rows(z, "z", (T,), E, u)
+        cu = seq = slot = init = sp = None
+        n, bs = 0, 1
+        if m is not None:
+            cu, seq, slot, init, n = _map(m, T, dev)
+            bs = m.block_tokens
+            sp = _status(status, on)
+        nslots = states.shape[0]
+        st = libssd.ssd_diag_state_update(_dense(states, "states", f32, (nslots, E, N), dev), up, us, dp, ds, zp, zs, pB, pC, bcs,
+                                          _dense(A, "A", f32, (E, N), dev), _dense(dt_bias, "dt_bias", f32, (E,), dev),
+                                          _dense(D, "D", f32, (E,), dev), _dense(y, "y", u.dtype, (T, E), dev), cu, seq, slot, init, n,
+                                          T, E, N, G, bs, nslots, _dtype_code(u), sp, on.handle)
+        libssd.check("ssd_diag_state_update", st)
+    return y
