@@ -179,6 +179,31 @@ SSD_API ssd_status_t ssd_diag_scan_fwd_varlen(const void* u, int64_t u_stride, c
                                               int32_t* status, cudaStream_t stream);
 
 /*
+ * Gradients through ssd_diag_scan_fwd, given dy = dLoss/dy and dfinal =
+ * dLoss/d(final_state).
+ *
+ *   inputs as the forward call's; dy [b][L][E] dtype; dfinal [b][E][N]
+ *          float32 or NULL (zero)
+ *   du, ddt_raw, dz [b][L][E] dtype, written (dz exactly when z is given)
+ *   dB, dC [b][L][G][N] dtype, written (summed over each group's channels)
+ *   dA [E][N], dD, ddt_bias [E] float32, written (summed over the batch)
+ *   dinit  [b][E][N] float32, written, may be NULL (not wanted)
+ *   workspace  ssd_diag_scan_bwd_workspace_bytes(...) bytes: states every 8
+ *          tokens and partial sums, no initial contents
+ * Deterministic: no atomics.  b == 0 or L == 0 zeroes dA, dD and ddt_bias
+ * and copies dfinal (or zeros) into dinit.
+ */
+SSD_API size_t ssd_diag_scan_bwd_workspace_bytes(int b, int L, int E, int N, int G);
+SSD_API ssd_status_t ssd_diag_scan_bwd(const void* u, int64_t u_stride, const void* dt_raw, int64_t dt_stride,
+                                       const void* z, int64_t z_stride, const void* B, const void* C,
+                                       int64_t bc_stride, const float* A, const float* dt_bias, const float* D,
+                                       const float* init_state, const void* dy, const float* dfinal, void* du,
+                                       void* ddt_raw, void* dz, void* dB, void* dC, float* dA, float* dD,
+                                       float* ddt_bias, float* dinit, int b, int L, int E, int N, int G,
+                                       ssd_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+
+/*
  * One token per request: the recurrence once, from slot init_slot[r] to the
  * slot of the token's block, r = seq_of[i] for row i.  The map's arrays may
  * all be NULL: row i is then state i, in place (nslots >= rows).

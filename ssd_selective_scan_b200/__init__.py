@@ -10,12 +10,12 @@ raises.
 from .layer import (chunk_scan_bwd, chunk_scan_bwd_workspace_bytes, chunk_scan_fwd, chunk_scan_fwd_varlen, chunk_scan_varlen_workspace_bytes,
                     chunk_scan_workspace_bytes, conv1d_silu, conv_scan_fwd, conv_scan_workspace_bytes,
                     decode_step, layer_prefill, split_channels, state_update)
-from .diag import (StateMap, conv1d_silu_bwd, conv1d_silu_varlen, diag_scan_fwd, diag_scan_fwd_varlen, diag_scan_workspace_bytes,
+from .diag import (StateMap, conv1d_silu_bwd, conv1d_silu_varlen, diag_scan_bwd, diag_scan_fwd, diag_scan_fwd_varlen, diag_scan_workspace_bytes,
                    diag_state_update, state_map)
 from .binding import SsdError
 
 __all__ = ["chunk_scan_bwd", "chunk_scan_bwd_workspace_bytes", "chunk_scan_fwd", "chunk_scan_fwd_varlen", "chunk_scan_varlen_workspace_bytes",
            "chunk_scan_workspace_bytes", "conv1d_silu", "conv_scan_fwd", "conv_scan_workspace_bytes",
-           "decode_step", "StateMap", "conv1d_silu_bwd", "conv1d_silu_varlen", "diag_scan_fwd", "diag_scan_fwd_varlen",
+           "decode_step", "StateMap", "conv1d_silu_bwd", "conv1d_silu_varlen", "diag_scan_bwd", "diag_scan_fwd", "diag_scan_fwd_varlen",
            "diag_scan_workspace_bytes", "diag_state_update", "state_map",
            "layer_prefill", "split_channels", "state_update", "SsdError"]

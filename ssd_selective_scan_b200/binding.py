@@ -71,6 +71,8 @@ DIAG_SIGNATURES = {
     "ssd_diag_scan_fwd": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 6 + [_i] * 6 + [_vp, _sz, _vp]),
     "ssd_diag_scan_fwd_varlen": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 9 + [_i] * 8 +
                                  [_vp, _sz, _vp, _vp]),
+    "ssd_diag_scan_bwd_workspace_bytes": (_sz, [_i] * 5),
+    "ssd_diag_scan_bwd": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 15 + [_i] * 6 + [_vp, _sz, _vp]),
     "ssd_diag_state_update": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 8 + [_i] * 8 + [_vp, _vp]),
 }
 
@@ -258,6 +260,18 @@ def ssd_diag_scan_fwd_varlen(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, 
     return load().ssd_diag_scan_fwd_varlen(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D,
                                            states, y, cu_seqlens, seq_of, slot_of, init_slot, nseq, T, E, N, G,
                                            block_tokens, nslots, dtype, workspace, workspace_bytes, status, stream)
+
+
+def ssd_diag_scan_bwd_workspace_bytes(b, L, E, N, G) -> int:
+    return load().ssd_diag_scan_bwd_workspace_bytes(b, L, E, N, G)
+
+
+def ssd_diag_scan_bwd(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D, init_state, dy, dfinal, du,
+                      ddt_raw, dz, dB, dC, dA, dD, ddt_bias, dinit, b, L, E, N, G, dtype, workspace, workspace_bytes,
+                      stream) -> int:
+    return load().ssd_diag_scan_bwd(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D, init_state,
+                                    dy, dfinal, du, ddt_raw, dz, dB, dC, dA, dD, ddt_bias, dinit, b, L, E, N, G, dtype,
+                                    workspace, workspace_bytes, stream)
 
 
 def ssd_diag_state_update(states, u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D, y,

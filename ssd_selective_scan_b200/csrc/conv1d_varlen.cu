@@ -29,7 +29,7 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
 {
     const int c0 = (blockIdx.y * kThreads + threadIdx.x) * kCpt;
     Piece p;
-    if (!find_piece<true>(blockIdx.x, sl, sl.nseq, 0, rows, kPiece, K - 2, p) || c0 >= E) return;
+    if (!find_piece_packed(blockIdx.x, sl, rows, kPiece, K - 2, p) || c0 >= E) return;
     const T* xb = x + c0;
     const bool head = p.t0 == p.s0;
     const int init = head ? sl.init_slot[p.r] : -1;

@@ -120,50 +120,59 @@ __device__ inline int slot_at(const Slots& s, int64_t flat)
     return (int)(flat / s.block);
 }
 
-// One piece of one sequence: the tokens t0 .. t1-1 of the rows, in sequence
-// r = [s0, s1).  Pieces are cut at the multiples of `seg` along the packed
-// rows, so that each is found from its index alone: index q < nseq is
-// sequence q's first piece, index nseq + m - 1 the piece that starts at row
-// m * seg where that row lies inside a sequence.  A row nearer than `keep` to
-// its sequence's start begins no piece (the first piece runs on over it).
+// One piece of one sequence: the rows t0 .. t1-1 of sequence r = [s0, s1).
+// The pieces of a sequence are numbered first, next, next + 1, ..; idx is this
+// one's.
 struct Piece {
     int r, t0, t1, s0, s1;
+    int64_t idx, first, next;
 };
 
-template <bool PACKED>
-__device__ inline bool find_piece(int q, const Slots& sl, int nseq, int L, int rows, int seg, int keep, Piece& p)
+// Dense sequences of L rows are cut every seg rows: piece q is the
+// (q % per)-th of sequence q / per.
+__host__ __device__ inline int pieces_per(int L, int seg) { return (int)(((int64_t)L + seg - 1) / seg); }
+
+__device__ inline bool find_piece_dense(int q, int L, int seg, Piece& p)
+{
+    const int per = pieces_per(L, seg);
+    p.r = q / per;
+    const int j = q - p.r * per;
+    p.s0 = p.r * L;
+    p.s1 = p.s0 + L;
+    p.t0 = p.s0 + j * seg;
+    p.t1 = j + 1 < per ? p.t0 + seg : p.s1;
+    p.idx = q;
+    p.first = (int64_t)p.r * per;
+    p.next = p.first + 1;
+    return true;
+}
+
+// Packed sequences are cut at the multiples of seg along the packed rows, so
+// that each piece is found from its index alone: index q < nseq is sequence
+// q's first piece, index nseq + m - 1 the piece that starts at row m * seg
+// where that row lies inside a sequence.  A row at most `keep` rows behind its
+// sequence's start begins no piece (the first piece runs on over it).
+__device__ inline bool find_piece_packed(int q, const Slots& sl, int rows, int seg, int keep, Piece& p)
 {
     auto bounds = [&](int r) {
-        if constexpr (PACKED) {
-            p.s0 = sl.cu[r];
-            p.s1 = sl.cu[r + 1];
-            if (p.s0 < 0 || p.s1 < p.s0 || p.s1 > rows) {
-                flag_invalid(sl.status);
-                return false;
-            }
-        } else {
-            p.s0 = r * L;
-            p.s1 = p.s0 + L;
-        }
         p.r = r;
-        return true;
+        p.s0 = sl.cu[r];
+        p.s1 = sl.cu[r + 1];
+        if (p.s0 >= 0 && p.s1 >= p.s0 && p.s1 <= rows) return true;
+        flag_invalid(sl.status);
+        return false;
     };
-    if (q < nseq) {
+    if (q < sl.nseq) {
         if (!bounds(q) || p.s1 == p.s0) return false;
         p.t0 = p.s0;
     } else {
-        const int64_t at = (int64_t)(q - nseq + 1) * seg;
+        const int64_t at = (int64_t)(q - sl.nseq + 1) * seg;
         if (at >= rows) return false;
-        int r;
-        if constexpr (PACKED) {
-            r = sl.seq_of[at];
-            if (r < 0) return false;       // behind the last sequence
-            if (r >= nseq) {
-                flag_invalid(sl.status);
-                return false;
-            }
-        } else {
-            r = (int)(at / L);
+        const int r = sl.seq_of[at];
+        if (r < 0) return false;       // behind the last sequence
+        if (r >= sl.nseq) {
+            flag_invalid(sl.status);
+            return false;
         }
         if (!bounds(r)) return false;
         if (at < p.s0 || at >= p.s1) {
@@ -176,6 +185,9 @@ __device__ inline bool find_piece(int q, const Slots& sl, int nseq, int L, int r
     int64_t cut = ((int64_t)p.t0 / seg + 1) * seg;
     if (p.t0 == p.s0 && cut - p.s0 <= keep) cut += seg;
     p.t1 = (int)(cut < p.s1 ? cut : p.s1);
+    p.idx = q;
+    p.first = p.r;
+    p.next = sl.nseq + p.s0 / seg;
     return true;
 }
 

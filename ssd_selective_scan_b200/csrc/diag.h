@@ -51,10 +51,24 @@ struct DiagArgs {
     bool bf16;
     SlotArgs sl;
     void* ws;
+    float* ckpt = nullptr;
 };
 size_t diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G);
 cudaError_t launch_diag_scan(const DiagArgs& a, cudaStream_t s);
 cudaError_t launch_diag_update(const DiagArgs& a, cudaStream_t s);
+
+// The states before every kDiagCkpt-th row of each sequence, for the backward
+// pass, to a.ckpt [nseq][ckpts_of(L)][E][N]; rows cut every seg rows (a
+// multiple of kDiagCkpt; L or more: not at all).  A cut walk leaves every
+// piece's final state and sum of dt in a.ws, diag_cut_bytes(...) bytes: [piece]
+// [E][N], then [piece][E], then the sequences' initial states.
+constexpr int kDiagCkpt = 8;
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int64_t ckpts_of(int L) { return ((int64_t)L + kDiagCkpt - 1) / kDiagCkpt; }
+size_t diag_cut_bytes(int nseq, int64_t pieces, int E, int N);
+cudaError_t launch_diag_ckpt(const DiagArgs& a, int seg, cudaStream_t s);
 
 struct DiagBwdArgs {
     DiagArgs f;            // the forward call's inputs

@@ -251,6 +251,53 @@ ssd_status_t ssd_diag_scan_fwd_varlen(const void* u, int64_t u_stride, const voi
     return from_cuda(launch_diag_scan(a, stream));
 }
 
+size_t ssd_diag_scan_bwd_workspace_bytes(int b, int L, int E, int N, int G)
+{
+    if (b <= 0 || L <= 0 || E <= 0 || N <= 0 || N > 64 || G <= 0 || E % G) return 0;
+    return diag_scan_bwd_workspace_bytes(b, L, E, N, G);
+}
+
+ssd_status_t ssd_diag_scan_bwd(const void* u, int64_t u_stride, const void* dt_raw, int64_t dt_stride, const void* z,
+                               int64_t z_stride, const void* B, const void* C, int64_t bc_stride, const float* A,
+                               const float* dt_bias, const float* D, const float* init_state, const void* dy,
+                               const float* dfinal, void* du, void* ddt_raw, void* dz, void* dB, void* dC, float* dA,
+                               float* dD, float* ddt_bias, float* dinit, int b, int L, int E, int N, int G,
+                               ssd_dtype_t dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (b < 0 || L < 0) return SSD_ERR_INVALID_ARG;
+    if ((int64_t)b * L > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    DiagArgs f{u, dt_raw, z, B, C, u_stride, dt_stride, z_stride, bc_stride, A, dt_bias, D, init_state, nullptr, nullptr,
+               b, L, b * L, E, N, G, dtype == SSD_BF16, SlotArgs{}, workspace};
+    const ssd_status_t st = check_scan(f, dtype);
+    if (st != SSD_OK) return st;
+    const bool tokens = f.rows > 0;
+    if (!dA || !dD || !ddt_bias || (tokens && (!dy || !du || !ddt_raw || !dB || !dC || (z && !dz)))) return SSD_ERR_INVALID_ARG;
+    const int e = elem_bytes(dtype);
+    if (!all_aligned({dy, dfinal, du, ddt_raw, dz, dA, dinit, workspace}, 16) || !all_aligned({dB, dC}, e) ||
+        !all_aligned({dD, ddt_bias}, 4))
+        return SSD_ERR_INVALID_ARG;
+    const size_t need = ssd_diag_scan_bwd_workspace_bytes(b, L, E, N, G);
+    if (workspace_bytes < need || (need && !workspace)) return SSD_ERR_INVALID_ARG;
+    const ScanRanges r = scan_ranges(f, e);
+    const int64_t io = (int64_t)f.rows * E * e, bc = (int64_t)f.rows * G * N * e, st_bytes = (int64_t)b * E * N * 4;
+    if (clash({span(du, io), span(ddt_raw, io), span(dz, z ? io : 0), span(dB, bc), span(dC, bc), span(dA, (int64_t)E * N * 4),
+               span(dD, (int64_t)E * 4), span(ddt_bias, (int64_t)E * 4), span(dinit, dinit ? st_bytes : 0), span(workspace, (int64_t)need)},
+              {r.u, r.dt, r.z, r.B, r.C, r.A, r.bias, r.D, span(dy, io), span(init_state, init_state ? st_bytes : 0),
+               span(dfinal, dfinal ? st_bytes : 0)}))
+        return SSD_ERR_INVALID_ARG;
+    if (!tokens) {
+        cudaError_t err = cudaMemsetAsync(dA, 0, (size_t)E * N * 4, stream);
+        if (err == cudaSuccess) err = cudaMemsetAsync(dD, 0, (size_t)E * 4, stream);
+        if (err == cudaSuccess) err = cudaMemsetAsync(ddt_bias, 0, (size_t)E * 4, stream);
+        if (err == cudaSuccess && dinit && b > 0)
+            err = dfinal ? cudaMemcpyAsync(dinit, dfinal, (size_t)st_bytes, cudaMemcpyDeviceToDevice, stream)
+                         : cudaMemsetAsync(dinit, 0, (size_t)st_bytes, stream);
+        return from_cuda(err);
+    }
+    const DiagBwdArgs a{f, dy, dfinal, du, ddt_raw, dz, dB, dC, dA, dD, ddt_bias, dinit};
+    return from_cuda(launch_diag_scan_bwd(a, stream));
+}
+
 ssd_status_t ssd_diag_state_update(float* states, const void* u, int64_t u_stride, const void* dt_raw,
                                    int64_t dt_stride, const void* z, int64_t z_stride, const void* B, const void* C,
                                    int64_t bc_stride, const float* A, const float* dt_bias, const float* D, void* y,

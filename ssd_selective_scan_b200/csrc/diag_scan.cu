@@ -24,7 +24,7 @@
 //
 // Few rows.  A lane's tokens are a serial chain, and a narrow layer's single
 // prompt has too few lanes to fill the device.  The rows are then cut into
-// pieces (find_piece): a first kernel walks every piece that has a successor
+// pieces (find_piece_dense, find_piece_packed): a first kernel walks every piece that has a successor
 // from a zero state (a sequence's first piece from its initial state) and
 // leaves its final state and the sum of its dt; a piece's true initial state
 // is then the fold of those before it, exp(A sum dt) h + h_local, which the
@@ -61,7 +61,6 @@ template <int LPC> struct Smem {
 struct CutWs {
     float *h, *sdt, *h0;
 };
-__host__ __device__ inline int64_t piece_count(int nseq, int rows, int seg) { return nseq + ((int64_t)rows - 1) / seg; }
 __host__ __device__ inline CutWs cut_ws(void* ws, int64_t pieces, int E, int N)
 {
     CutWs c;
@@ -70,12 +69,17 @@ __host__ __device__ inline CutWs cut_ws(void* ws, int64_t pieces, int E, int N)
     c.h0 = c.sdt + pieces * E;
     return c;
 }
+inline size_t cut_ws_bytes(int nseq, int64_t pieces, int E, int N) { return ((size_t)pieces * E * (N + 1) + (size_t)nseq * E * N) * 4; }
 
-// FULL: write y and the states.  Otherwise the piece's final state and sum of
-// dt go to the workspace.  CUT: the pieces' states are in the workspace.
-template <typename T, int LPC, bool PACKED, bool FULL, bool CUT>
-__global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, int seg)
+// What a walk leaves: a piece's final state and sum of dt (in the workspace),
+// y and the states, or the states every kDiagCkpt rows.
+enum Mode { kLocal, kOutput, kCkpt };
+
+// CUT: the pieces' states are in the workspace.
+template <typename T, int LPC, bool PACKED, Mode MODE, bool CUT>
+__global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, int seg, int64_t pieces)
 {
+    constexpr bool FULL = MODE == kOutput;
     using TL = Tile<LPC>;
     constexpr int CH = TL::CH, TT = TL::TT, VPR = TL::VPR, PAD = TL::PAD;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -83,8 +87,8 @@ __global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, i
 
     const Slots sl{a.sl.cu, a.sl.seq_of, a.sl.slot_of, a.sl.init_slot, a.sl.nseq, a.sl.nslots, a.sl.block, a.sl.status};
     Piece p;
-    if (!find_piece<PACKED>(blockIdx.x, sl, a.nseq, a.L, a.rows, seg, 0, p)) return;
-    if (!FULL && p.t1 == p.s1) return;   // no successor
+    if (!(PACKED ? find_piece_packed(blockIdx.x, sl, a.rows, seg, 0, p) : find_piece_dense(blockIdx.x, a.L, seg, p))) return;
+    if (MODE == kLocal && p.t1 == p.s1) return;   // no successor
 
     const int tid = threadIdx.x;
     const int q = tid % LPC, cl = tid / LPC;
@@ -120,19 +124,17 @@ __global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, i
         h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
     };
     auto store_h = [&](float* dst) { *reinterpret_cast<float4*>(dst) = make_float4(h[0], h[1], h[2], h[3]); };
-    const int64_t pieces = CUT ? piece_count(a.nseq, a.rows, seg) : 0;
     const CutWs ws = cut_ws(a.ws, pieces, a.E, a.N);
     const bool head = p.t0 == p.s0;
     if (live) {
-        if (!CUT || (head && (!FULL || p.t1 == p.s1))) {
+        if (!CUT || (head && (MODE == kLocal || p.t1 == p.s1))) {
             if (head && init_at >= 0) load_h(a.init + init_at * st_all + st);
-            if (CUT && !FULL && head) store_h(ws.h0 + p.r * st_all + st);
+            if (CUT && MODE == kLocal && head) store_h(ws.h0 + p.r * st_all + st);
         } else if (head) {
             load_h(ws.h0 + p.r * st_all + st);
-        } else if (FULL) {
-            load_h(ws.h + p.r * st_all + st);
-            for (int64_t at = (int64_t)(p.s0 / seg + 1) * seg; at < p.t0; at += seg) {
-                const int64_t i = a.nseq + at / seg - 1;
+        } else if (MODE != kLocal) {
+            load_h(ws.h + p.first * st_all + st);
+            for (int64_t i = p.next; i < p.idx; ++i) {
                 const float sdt = ws.sdt[i * a.E + e];
                 const float4 v = *reinterpret_cast<const float4*>(ws.h + i * st_all + st);
                 h[0] = fmaf(ex2(A2[0] * sdt), h[0], v.x);
@@ -220,6 +222,11 @@ __global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, i
         float2* dx = sm.dx[buf];
         const int groups = (min(TT, p.t1 - t) + 3) / 4;
         for (int gr = 0; gr < groups; ++gr) {
+            if constexpr (MODE == kCkpt) {
+                const int row = t + 4 * gr - p.s0;   // pieces start at multiples of kDiagCkpt
+                if (row % kDiagCkpt == 0 && live)
+                    store_h(a.ckpt + ((int64_t)p.r * ckpts_of(a.L) + row / kDiagCkpt) * st_all + st);
+            }
             float acc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -244,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, i
                         }
                         keep += sl.block;
                     }
-                } else {
+                } else if (MODE == kLocal) {
                     sdt += d.x;
                 }
             }
@@ -306,10 +313,9 @@ __global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, i
                 store_h(a.final_state + p.r * st_all + st);
             }
         }
-    } else if (live) {
-        const int64_t i = head ? p.r : a.nseq + p.t0 / seg - 1;
-        store_h(ws.h + i * st_all + st);
-        if (q == 0) ws.sdt[i * a.E + e] = sdt;
+    } else if (MODE == kLocal && live) {
+        store_h(ws.h + p.idx * st_all + st);
+        if (q == 0) ws.sdt[p.idx * a.E + e] = sdt;
     }
 }
 
@@ -331,43 +337,41 @@ int piece_rows(int nseq, int rows, int E, int N, int G)
     return seg < rows ? (int)seg : rows;
 }
 
-template <typename T, int LPC, bool PACKED>
-cudaError_t launch_lpc(const DiagArgs& a, cudaStream_t s)
+int64_t piece_count(bool packed, int nseq, int L, int rows, int seg)
 {
-    using TL = Tile<LPC>;
-    const int seg = piece_rows(a.nseq, a.rows, a.E, a.N, a.G);
-    const bool cut = seg < (PACKED ? a.rows : a.L);
-    const int per_group = a.E / a.G;
-    const unsigned tiles = (unsigned)((per_group + TL::CH - 1) / TL::CH * a.G);
-    const int smem = (int)sizeof(Smem<LPC>);
-    const int use = cut ? seg : 0x7fffffff;
-    const dim3 grid((unsigned)(cut ? piece_count(a.nseq, a.rows, seg) : a.nseq), tiles);
-    auto opt_in = [&](const void* f) {
-        return smem > 48 * 1024 ? cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
-    };
-    cudaError_t e;
-    if (cut) {
-        if ((e = opt_in((const void*)diag_scan_kernel<T, LPC, PACKED, false, true>)) != cudaSuccess) return e;
-        if ((e = opt_in((const void*)diag_scan_kernel<T, LPC, PACKED, true, true>)) != cudaSuccess) return e;
-        diag_scan_kernel<T, LPC, PACKED, false, true><<<grid, kThreads, smem, s>>>(a, use);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        diag_scan_kernel<T, LPC, PACKED, true, true><<<grid, kThreads, smem, s>>>(a, use);
-    } else {
-        if ((e = opt_in((const void*)diag_scan_kernel<T, LPC, PACKED, true, false>)) != cudaSuccess) return e;
-        diag_scan_kernel<T, LPC, PACKED, true, false><<<grid, kThreads, smem, s>>>(a, use);
-    }
+    return packed ? nseq + ((int64_t)rows - 1) / seg : (int64_t)nseq * pieces_per(L, seg);
+}
+
+template <typename T, int LPC, bool PACKED, Mode MODE, bool CUT>
+cudaError_t launch_mode(const DiagArgs& a, int seg, int64_t pieces, cudaStream_t s)
+{
+    constexpr int smem = (int)sizeof(Smem<LPC>);
+    static_assert(smem <= 48 * 1024, "no opt-in needed");
+    const int per_group = a.E / a.G, CH = Tile<LPC>::CH;
+    const dim3 grid((unsigned)pieces, (unsigned)((per_group + CH - 1) / CH * a.G));
+    diag_scan_kernel<T, LPC, PACKED, MODE, CUT><<<grid, kThreads, smem, s>>>(a, seg, pieces);
     return cudaGetLastError();
 }
 
-template <typename T, bool PACKED>
-cudaError_t launch_t(const DiagArgs& a, cudaStream_t s)
+template <typename T, int LPC, bool PACKED, Mode MODE>
+cudaError_t launch_lpc(const DiagArgs& a, int seg, cudaStream_t s)
+{
+    const bool cut = seg < (PACKED ? a.rows : a.L);
+    if (!cut) return launch_mode<T, LPC, PACKED, MODE, false>(a, 0x7fffffff, a.nseq, s);
+    const int64_t pieces = piece_count(PACKED, a.nseq, a.L, a.rows, seg);
+    const cudaError_t e = launch_mode<T, LPC, PACKED, kLocal, true>(a, seg, pieces, s);
+    return e != cudaSuccess ? e : launch_mode<T, LPC, PACKED, MODE, true>(a, seg, pieces, s);
+}
+
+template <typename T, bool PACKED, Mode MODE>
+cudaError_t launch_t(const DiagArgs& a, int seg, cudaStream_t s)
 {
     switch (diag_lanes(a.N)) {
-        case 1: return launch_lpc<T, 1, PACKED>(a, s);
-        case 2: return launch_lpc<T, 2, PACKED>(a, s);
-        case 4: return launch_lpc<T, 4, PACKED>(a, s);
-        case 8: return launch_lpc<T, 8, PACKED>(a, s);
-        default: return launch_lpc<T, 16, PACKED>(a, s);
+        case 1: return launch_lpc<T, 1, PACKED, MODE>(a, seg, s);
+        case 2: return launch_lpc<T, 2, PACKED, MODE>(a, seg, s);
+        case 4: return launch_lpc<T, 4, PACKED, MODE>(a, seg, s);
+        case 8: return launch_lpc<T, 8, PACKED, MODE>(a, seg, s);
+        default: return launch_lpc<T, 16, PACKED, MODE>(a, seg, s);
     }
 }
 
@@ -377,14 +381,22 @@ size_t diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G)
 {
     const int seg = piece_rows(nseq, rows, E, N, G);
     if (seg >= rows) return 0;
-    const size_t pieces = (size_t)piece_count(nseq, rows, seg);
-    return (pieces * E * (N + 1) + (size_t)nseq * E * N) * 4;
+    // packed or dense: a dense batch has at most one short piece per sequence
+    return cut_ws_bytes(nseq, nseq + ((int64_t)rows - 1) / seg + 1, E, N);
 }
 
 cudaError_t launch_diag_scan(const DiagArgs& a, cudaStream_t s)
 {
-    if (a.sl.cu) return a.bf16 ? launch_t<__nv_bfloat16, true>(a, s) : launch_t<float, true>(a, s);
-    return a.bf16 ? launch_t<__nv_bfloat16, false>(a, s) : launch_t<float, false>(a, s);
+    const int seg = piece_rows(a.nseq, a.rows, a.E, a.N, a.G);
+    if (a.sl.cu) return a.bf16 ? launch_t<__nv_bfloat16, true, kOutput>(a, seg, s) : launch_t<float, true, kOutput>(a, seg, s);
+    return a.bf16 ? launch_t<__nv_bfloat16, false, kOutput>(a, seg, s) : launch_t<float, false, kOutput>(a, seg, s);
 }
+
+cudaError_t launch_diag_ckpt(const DiagArgs& a, int seg, cudaStream_t s)
+{
+    return a.bf16 ? launch_t<__nv_bfloat16, false, kCkpt>(a, seg, s) : launch_t<float, false, kCkpt>(a, seg, s);
+}
+
+size_t diag_cut_bytes(int nseq, int64_t pieces, int E, int N) { return cut_ws_bytes(nseq, pieces, E, N); }
 
 }  // namespace ssd

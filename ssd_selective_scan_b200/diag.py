@@ -314,6 +314,39 @@ def diag_scan_fwd_varlen(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor,
     return y
 
 
+def diag_scan_bwd(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, dy: torch.Tensor, *,
+                  dt_bias: torch.Tensor | None = None, D: torch.Tensor | None = None, z: torch.Tensor | None = None,
+                  init_state: torch.Tensor | None = None, dfinal: torch.Tensor | None = None, want_dinit: bool = True,
+                  workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients through diag_scan_fwd.  Inputs as for the forward call; dy
+    [b, L, E] (I/O dtype), dfinal [b, E, N] f32 or None.  Returns dict(du,
+    ddt_raw, dz, dB, dC, dA, dD, ddt_bias, dinit): du, ddt_raw, dz [b, L, E]
+    and dB, dC [b, L, G, N] in the I/O dtype, the others f32; dz is None
+    without z, dinit if not wanted."""
+    if u.dim() != 3:
+        raise ValueError("u must be [b, L, E]")
+    b, L, E = u.shape
+    f32 = torch.float32
+    with _On(u, stream) as on:
+        dev = on.device
+        pB, pC, bcs, G, N = _bc(B, C, (b, L), u)
+        up, us = _rows(u, "u", (b, L), E, u)
+        dp, ds = _rows(dt_raw, "dt_raw", (b, L), E, u)
+        zp, zs = _rows(z, "z", (b, L), E, u)
+        io, bc = (lambda: on.empty((b, L, E), u.dtype)), (lambda: on.empty((b, L, G, N), u.dtype))
+        r = dict(du=io(), ddt_raw=io(), dz=None if z is None else io(), dB=bc(), dC=bc(), dA=on.empty((E, N), f32), dD=on.empty(E, f32),
+                 ddt_bias=on.empty(E, f32), dinit=on.empty((b, E, N), f32) if want_dinit else None)
+        wp, wb = on.workspace(workspace, int(libssd.ssd_diag_scan_bwd_workspace_bytes(b, L, E, N, G)))
+        st = libssd.ssd_diag_scan_bwd(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
+                                      _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
+                                      _dense(init_state, "init_state", f32, (b, E, N), dev), _dense(dy, "dy", u.dtype, (b, L, E), dev),
+                                      _dense(dfinal, "dfinal", f32, (b, E, N), dev), _ptr(r["du"]), _ptr(r["ddt_raw"]), _ptr(r["dz"]),
+                                      _ptr(r["dB"]), _ptr(r["dC"]), _ptr(r["dA"]), _ptr(r["dD"]), _ptr(r["ddt_bias"]), _ptr(r["dinit"]),
+                                      b, L, E, N, G, _dtype_code(u), wp, wb, on.handle)
+        libssd.check("ssd_diag_scan_bwd", st)
+    return r
+
+
 def diag_state_update(states: torch.Tensor, u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                       C: torch.Tensor, m: StateMap | None = None, *, dt_bias: torch.Tensor | None = None,
                       D: torch.Tensor | None = None, z: torch.Tensor | None = None, y: torch.Tensor | None = None,

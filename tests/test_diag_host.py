@@ -162,8 +162,45 @@ def test_update_without_a_map():
     assert packed("ssd_diag_state_update", nslots=29, **none) == INV      # fewer states than rows
 
 
+def bwd(**kw):
+    a = dict(u=fake(1), u_stride=64, dt_raw=fake(2), dt_stride=72, z=fake(3), z_stride=128, B=fake(4), C=fake(4, 64), bc_stride=64, A=fake(5),
+             dt_bias=None, D=None, init_state=fake(6), dy=fake(7), dfinal=fake(8), du=fake(9), ddt_raw=fake(10), dz=fake(11), dB=fake(12),
+             dC=fake(13), dA=fake(14), dD=fake(15), ddt_bias=fake(16), dinit=fake(17), b=2, L=30, E=64, N=16, G=2, dtype=BF16,
+             workspace=fake(18), workspace_bytes=1 << 24, stream=None)
+    a.update(kw)
+    return libssd.ssd_diag_scan_bwd(**a)
+
+
+def test_scan_bwd_validation():
+    for k in ("u", "dt_raw", "B", "C", "A", "dy", "du", "ddt_raw", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "workspace"):
+        assert bwd(**{k: None}) == INV, k
+    assert bwd(b=-1) == INV and bwd(L=-1) == INV and bwd(G=3) == INV and bwd(N=2) == INV and bwd(dtype=7) == INV
+    need = libssd.ssd_diag_scan_bwd_workspace_bytes(2, 30, 64, 16, 2)
+    assert need > 0 and bwd(workspace_bytes=need - 1) == INV and bwd(workspace=fake(18, 8)) == INV
+    assert bwd(du=fake(1)) == INV and bwd(dA=fake(5)) == INV and bwd(dinit=fake(6)) == INV and bwd(dB=fake(9, 32)) == INV
+    assert bwd(workspace=fake(7)) == INV and bwd(dy=fake(7, 8)) == INV and bwd(dz=fake(11, 2)) == INV
+    assert bwd(N=68, bc_stride=136) == UNS
+    assert libssd.ssd_diag_scan_bwd_workspace_bytes(2, 0, 64, 16, 2) == 0 and libssd.ssd_diag_scan_bwd_workspace_bytes(2, 5, 64, 68, 2) == 0
+
+
 # ---------------------------------------------------------------------------
 # the references themselves
+
+
+def test_reference_gradients_against_differences():
+    """Autograd through the float64 definitions, which the GPU gradients are
+    held to, against central differences (torch.autograd.gradcheck)."""
+    p = R.f64(R.scan_inputs((5,), 8, 4, 1, torch.float32, seed=3))
+    keys = list(p)
+    leaves = [p[k].clone().requires_grad_() for k in keys] + [torch.randn(8, 4, dtype=torch.float64, requires_grad=True)]
+
+    def run(*v):
+        y, h = R.scan(dict(zip(keys, v[:-1])), v[-1])
+        return y, h[-1]
+    assert torch.autograd.gradcheck(run, leaves)
+    w = torch.randn(3, 4, dtype=torch.float64, requires_grad=True)
+    ext = torch.randn(9, 3, dtype=torch.float64, requires_grad=True)
+    assert torch.autograd.gradcheck(lambda e, v, b: R.conv(e, v, b), (ext, w, torch.randn(3, dtype=torch.float64, requires_grad=True)))
 
 
 def test_reference_step_by_hand():
