@@ -26,7 +26,8 @@
  *   - B, C have the element type `dtype`, token t, group g, n at
  *     B[t*bc_stride + g*N + n]; any element-aligned pointer and any stride of
  *     at least G*N (they are usually columns of a projection's rows).
- *   - A [E][N], D [E], dt_bias [E], conv weights and states are float32;
+ *   - A [E][N], D [E], dt_bias [E], conv weights (16-byte aligned, as A) and
+ *     states are float32;
  *     sums, states and gradients accumulate in float32.  A is expected <= 0.
  *   - N is a multiple of 4, at most 64 (else SSD_ERR_UNSUPPORTED above 64).
  *

@@ -89,6 +89,8 @@ class SsdError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load libssd.so (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

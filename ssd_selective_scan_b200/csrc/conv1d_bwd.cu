@@ -41,106 +41,155 @@ conv1d_bwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const fl
     const T* gb = dout + row0 * E + c0;
     T* dxb = dx + row0 * E + c0;
 
-    float wt[K][kCpt], bs[kCpt], dw[K][kCpt], db[kCpt];
+    // 4 channels as two fp32 pairs
+    float2 wt[K][2], bs[2], dw[K][2], db[2];
+    {
+        float v[K][kCpt];
+        load_taps<K>(w + (size_t)c0 * K, v);
 #pragma unroll
-    for (int c = 0; c < kCpt; ++c) {
-        bs[c] = bias ? bias[c0 + c] : 0.0f;
-        db[c] = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+            bs[h] = bias ? make_float2(bias[c0 + 2 * h], bias[c0 + 2 * h + 1]) : make_float2(0.0f, 0.0f);
+            db[h] = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            wt[j][c] = __ldg(w + (size_t)(c0 + c) * K + j);
-            dw[j][c] = 0.0f;
+            for (int j = 0; j < K; ++j) {
+                wt[j][h] = make_float2(v[j][2 * h], v[j][2 * h + 1]);
+                dw[j][h] = make_float2(0.0f, 0.0f);
+            }
         }
     }
-    float hist[K][kCpt], ds[K][kCpt];   // ds[j]: ds of the row j before this one
+    // x[j]: the input j rows before this one; ds[j] likewise
+    float2 xr[K][2], ds[K][2];
+    auto pairs = [](const Row4<T>& q, float2 (&o)[2]) {
+        float v[kCpt];
+        q.get(v);
+        o[0] = make_float2(v[0], v[1]);
+        o[1] = make_float2(v[2], v[3]);
+    };
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-#pragma unroll
-        for (int c = 0; c < kCpt; ++c) hist[j][c] = ds[j][c] = 0.0f;
+    for (int j = 0; j < K; ++j) xr[j][0] = xr[j][1] = ds[j][0] = ds[j][1] = make_float2(0.0f, 0.0f);
     if (t0 > 0) {   // t0 >= kTile >= K: the rows before are there
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
             Row4<T> q;
-            q.load(xb + (int64_t)(t0 - (K - 1) + j) * E);
-            q.get(hist[j]);
+            q.load(xb + (int64_t)(t0 - 1 - j) * E);
+            pairs(q, xr[j]);
         }
     } else if (conv_state) {
         Cache4<T, K> old;
         old.load(conv_state + ((int64_t)bi * E + c0) * K);
 #pragma unroll
-        for (int j = 1; j < K; ++j)
-#pragma unroll
-            for (int c = 0; c < kCpt; ++c) hist[j - 1][c] = old.get(c, j);
+        for (int j = 0; j < K - 1; ++j) {
+            xr[j][0] = make_float2(old.get(0, K - 1 - j), old.get(1, K - 1 - j));
+            xr[j][1] = make_float2(old.get(2, K - 1 - j), old.get(3, K - 1 - j));
+        }
     }
     Cache4<T, K> dcache;
 #pragma unroll
     for (int i = 0; i < Cache4<T, K>::kWords; ++i) dcache.w[i] = 0;
 
-    for (int tb = t0; tb < t1 + K - 1; tb += kGroup) {
-        Row4<T> rx[kGroup], rg[kGroup];
+    auto shift = [](float2 (&v)[K][2]) {
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
-            if (tb + u < t1 + K - 1 && tb + u < L) {
-                rx[u].load(xb + (int64_t)(tb + u) * E);
-                rg[u].load(gb + (int64_t)(tb + u) * E);
-            }
+        for (int j = K - 1; j > 0; --j) {
+            v[j][0] = v[j - 1][0];
+            v[j][1] = v[j - 1][1];
+        }
+    };
+    // Row t is taken in: ds_t and, where the tile owns it, its part of dw, db
+    auto take = [&](const Row4<T>& qx, const Row4<T>& qg, bool own) {
+        shift(xr);
+        shift(ds);
+        float2 g[2];
+        pairs(qx, xr[0]);
+        pairs(qg, g);
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            const int t = tb + u;
-            if (t >= t1 + K - 1) break;
+        for (int h = 0; h < 2; ++h) {
+            float2 v = bs[h];
 #pragma unroll
-            for (int j = K - 1; j > 0; --j)
+            for (int j = 0; j < K; ++j) v = pk_fma(wt[j][h], xr[K - 1 - j][h], v);
+            // SiLU'(v) = sg (1 + v (1 - sg)) = sg + (v sg) (1 - sg)
+            const float2 sg = make_float2(sigmoid_f(v.x), sigmoid_f(v.y));
+            const float2 d = pk_fma(pk_mul(v, sg), pk_fma(sg, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f)), sg);
+            ds[0][h] = pk_mul(g[h], d);
+            if (own) {
+                db[h] = make_float2(db[h].x + ds[0][h].x, db[h].y + ds[0][h].y);
 #pragma unroll
-                for (int c = 0; c < kCpt; ++c) ds[j][c] = ds[j - 1][c];
-            if (t < L) {
-                float gv[kCpt];
-                rx[u].get(hist[K - 1]);
-                rg[u].get(gv);
-#pragma unroll
-                for (int c = 0; c < kCpt; ++c) {
-                    float v = bs[c];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) v = fmaf(wt[j][c], hist[j][c], v);
-                    ds[0][c] = gv[c] * dsilu_f(v, sigmoid_f(v));
-                    if (t < t1) {
-                        db[c] += ds[0][c];
-#pragma unroll
-                        for (int j = 0; j < K; ++j) dw[j][c] = fmaf(ds[0][c], hist[j][c], dw[j][c]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kCpt; ++c) ds[0][c] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                for (int c = 0; c < kCpt; ++c) hist[j][c] = hist[j + 1][c];
-            const int to = t - (K - 1);   // the row whose dx is now complete
-            float o[kCpt];
-#pragma unroll
-            for (int c = 0; c < kCpt; ++c) {
-                o[c] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < K; ++j) o[c] = fmaf(wt[j][c], ds[j][c], o[c]);
-            }
-            if (to >= t0) {
-                Row4<T>::store(dxb + (int64_t)to * E, o);
-            } else if (to < 0) {          // a cached column: to + K, in 1 .. K-1
-#pragma unroll
-                for (int j = 1; j < K; ++j)
-                    if (j == to + K)
-#pragma unroll
-                        for (int c = 0; c < kCpt; ++c) dcache.set(c, j, o[c]);
+                for (int j = 0; j < K; ++j) dw[j][h] = pk_fma(ds[0][h], xr[K - 1 - j][h], dw[j][h]);
             }
         }
+    };
+    // dx of the row K - 1 before the last one taken in
+    auto give = [&](float (&o)[kCpt]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float2 v = pk_mul(wt[0][h], ds[0][h]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) v = pk_fma(wt[j][h], ds[j][h], v);
+            o[2 * h] = v.x;
+            o[2 * h + 1] = v.y;
+        }
+    };
+    auto put = [&](int t) {
+        const int to = t - (K - 1);
+        float o[kCpt];
+        give(o);
+        if (to >= t0) {
+            Row4<T>::store(dxb + (int64_t)to * E, o);
+        } else if (to < 0) {          // a cached column: to + K, in 1 .. K-1
+#pragma unroll
+            for (int j = 1; j < K; ++j)
+                if (j == to + K)
+#pragma unroll
+                    for (int c = 0; c < kCpt; ++c) dcache.set(c, j, o[c]);
+        }
+    };
+
+    Row4<T> rx[kGroup], rg[kGroup];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            rx[u].load(xb + (int64_t)(t + u) * E);
+            rg[u].load(gb + (int64_t)(t + u) * E);
+        }
+    };
+    int t = t0;
+    if (t + kGroup <= t1) {
+        fetch(t);
+        while (true) {
+            Row4<T> nx[kGroup], ng[kGroup];
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                nx[u] = rx[u];
+                ng[u] = rg[u];
+            }
+            const bool more = t + 2 * kGroup <= t1;
+            if (more) fetch(t + kGroup);
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                take(nx[u], ng[u], true);
+                put(t + u);
+            }
+            t += kGroup;
+            if (!more) break;
+        }
+    }
+    for (; t < t1 + K - 1; ++t) {
+        if (t < L) {
+            Row4<T> qx, qg;
+            qx.load(xb + (int64_t)t * E);
+            qg.load(gb + (int64_t)t * E);
+            take(qx, qg, t < t1);
+        } else {
+            shift(ds);
+            ds[0][0] = ds[0][1] = make_float2(0.0f, 0.0f);
+        }
+        put(t);
     }
     if (t0 == 0 && dconv_state) dcache.store(dconv_state + ((int64_t)bi * E + c0) * K);
     // [tile][K + 1][E]: taps, then the bias
     float* pr = part + (int64_t)blockIdx.x * (K + 1) * E + c0;
 #pragma unroll
-    for (int j = 0; j < K; ++j) *reinterpret_cast<float4*>(pr + (int64_t)j * E) = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-    *reinterpret_cast<float4*>(pr + (int64_t)K * E) = make_float4(db[0], db[1], db[2], db[3]);
+    for (int j = 0; j < K; ++j) *reinterpret_cast<float4*>(pr + (int64_t)j * E) = make_float4(dw[j][0].x, dw[j][0].y, dw[j][1].x, dw[j][1].y);
+    *reinterpret_cast<float4*>(pr + (int64_t)K * E) = make_float4(db[0].x, db[0].y, db[1].x, db[1].y);
 }
 
 // Sum over the tiles: 32 columns x 8 lanes of tiles per CTA, the lanes joined

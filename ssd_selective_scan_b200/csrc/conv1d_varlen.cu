@@ -40,11 +40,8 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
 
     float wt[K][kCpt], bs[kCpt];
 #pragma unroll
-    for (int c = 0; c < kCpt; ++c) {
-        bs[c] = bias ? bias[c0 + c] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) wt[j][c] = __ldg(w + (size_t)(c0 + c) * K + j);
-    }
+    for (int c = 0; c < kCpt; ++c) bs[c] = bias ? bias[c0 + c] : 0.0f;
+    load_taps<K>(w + (size_t)c0 * K, wt);
 
     // hist[j]: the input K - 1 - j rows before the next one
     float hist[K][kCpt];

@@ -52,4 +52,20 @@ template <typename T, int K> struct Cache4 {
     __device__ void set(int c, int j, float v) { io<T>::word_set(w, c * K + j, v); }
 };
 
+// The taps of a thread's 4 channels: 4 * K adjacent floats, K vectors.
+template <int K>
+__device__ inline void load_taps(const float* w, float (&wt)[K][4])
+{
+    float v[4 * K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(w) + i);
+        v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < K; ++j) wt[j][c] = v[c * K + j];
+}
+
 }  // namespace ssd

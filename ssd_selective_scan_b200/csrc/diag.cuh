@@ -63,6 +63,28 @@ __device__ inline float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + __ex
 // d SiLU(v) / dv, given sigmoid(v)
 __device__ inline float dsilu_f(float v, float sg) { return sg * fmaf(v, 1.0f - sg, 1.0f); }
 
+// Sums of v[0 .. NV) over LANES lanes (STRIDE apart), each lane keeping a part:
+// v[i] ends as the sum of value `first + i`, i < max(1, NV / LANES).
+template <int NV, int LANES, int STRIDE>
+__device__ inline void scatter_sum(float* v, int l, int& first)
+{
+    if constexpr (LANES > 1) {
+        if constexpr (NV > 1) {
+            const bool up = l & (LANES / 2);
+#pragma unroll
+            for (int i = 0; i < NV / 2; ++i) {
+                const float keep = up ? v[NV / 2 + i] : v[i], send = up ? v[i] : v[NV / 2 + i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, LANES / 2 * STRIDE);
+            }
+            if (up) first += NV / 2;
+            scatter_sum<NV / 2, LANES / 2, STRIDE>(v, l, first);
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], LANES / 2 * STRIDE);
+            scatter_sum<1, LANES / 2, STRIDE>(v, l, first);
+        }
+    }
+}
+
 // 8 adjacent elements as they lie in memory: 16 bytes (bf16) or 32 (f32).
 template <typename T> struct Raw8 {
     uint4 q[sizeof(T) / 2];

@@ -141,7 +141,7 @@ ssd_status_t ssd_conv1d_silu_varlen(const void* x, int64_t x_stride, void* out, 
     if (st != SSD_OK) return st;
     if (T > 0 && (!x || !out || !w || (nslots > 0 && !cache))) return SSD_ERR_INVALID_ARG;
     if (x_stride % 8 || x_stride < E || out_stride % 8 || out_stride < E) return SSD_ERR_INVALID_ARG;
-    if (!all_aligned({x, out, cache}, 16) || !all_aligned({w, bias}, 4)) return SSD_ERR_INVALID_ARG;
+    if (!all_aligned({x, out, cache, w}, 16) || !aligned(bias, 4)) return SSD_ERR_INVALID_ARG;
     const int e = elem_bytes(dtype);
     const MapRanges m = map_ranges(sl, T);
     if (clash({rows_span(out, T, out_stride, E, e), span(cache, (int64_t)nslots * E * k * e), m.status},
@@ -167,7 +167,7 @@ ssd_status_t ssd_conv1d_silu_bwd(const void* x, const float* w, const float* bia
     if (!valid_dtype(dtype) || b < 0 || L < 0 || E <= 0 || E % 8 || k <= 0) return SSD_ERR_INVALID_ARG;
     const bool tokens = b > 0 && L > 0;
     if (!dw || (tokens && (!x || !w || !dout || !dx))) return SSD_ERR_INVALID_ARG;
-    if (!all_aligned({x, dout, dx, conv_state, dconv_state, workspace}, 16) || !all_aligned({w, bias, dw, dbias}, 4))
+    if (!all_aligned({x, dout, dx, conv_state, dconv_state, workspace, w}, 16) || !all_aligned({bias, dw, dbias}, 4))
         return SSD_ERR_INVALID_ARG;
     const size_t need = ssd_conv1d_silu_bwd_workspace_bytes(b, L, E, k);
     if (workspace_bytes < need || (need && !workspace)) return SSD_ERR_INVALID_ARG;

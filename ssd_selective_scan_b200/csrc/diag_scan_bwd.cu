@@ -69,28 +69,6 @@ template <typename T, int LPC> struct Smem {
     T raw[2][4][TL::TT][TL::CH];              // u, dt_raw, dy, z
 };
 
-// Sums of v[0 .. NV) over LANES lanes (STRIDE apart), each lane keeping a part:
-// v[i] ends as the sum of value `first + i`, i < max(1, NV / LANES).
-template <int NV, int LANES, int STRIDE>
-__device__ inline void scatter_sum(float* v, int l, int& first)
-{
-    if constexpr (LANES > 1) {
-        if constexpr (NV > 1) {
-            const bool up = l & (LANES / 2);
-#pragma unroll
-            for (int i = 0; i < NV / 2; ++i) {
-                const float keep = up ? v[NV / 2 + i] : v[i], send = up ? v[i] : v[NV / 2 + i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, LANES / 2 * STRIDE);
-            }
-            if (up) first += NV / 2;
-            scatter_sum<NV / 2, LANES / 2, STRIDE>(v, l, first);
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], LANES / 2 * STRIDE);
-            scatter_sum<1, LANES / 2, STRIDE>(v, l, first);
-        }
-    }
-}
-
 __device__ inline void cp16(void* smem, const void* gmem)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");

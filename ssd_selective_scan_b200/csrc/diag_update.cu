@@ -3,10 +3,14 @@
 //
 // HBM-bound: 8 bytes of state move per element (4 in, 4 out) for one
 // exponential and four FMAs.  LPC lanes share a channel, 4 states (16 bytes)
-// each, so a warp reads and writes 512 adjacent bytes of a state.  A thread
-// keeps its channel's A, D and dt_bias and walks kRows rows, all of whose
-// state loads are issued before the first is used: the parameters are read
-// once per kRows rows, and each thread has kRows x 16 bytes in flight.
+// each, so a warp reads and writes 512 adjacent bytes of a state.  A CTA
+// takes CH = 128 / LPC channels of kUpdRows rows: each thread first issues
+// its kUpdRows state loads (128 bytes in flight per thread), and while those
+// are on their way the CTA forms dt and x = dt u once per (row, channel) and
+// lays them and the rows' B and C out in shared memory, so that the lanes of
+// a channel do not each load and compute them again.  A, D and dt_bias are
+// read once for the rows.  y's sums over a channel's lanes are exchanged for
+// all rows at once, each lane ending with some of the rows.
 #include "diag.cuh"
 #include "diag.h"
 
@@ -19,22 +23,16 @@ constexpr int kUpdRows = 8;
 template <typename T, int LPC, int ROWS>
 __global__ void __launch_bounds__(kUpdThreads) diag_update_kernel(const DiagArgs a)
 {
-    constexpr int CH = kUpdThreads / LPC;
-    const int q = threadIdx.x % LPC;
-    const int e = blockIdx.y * CH + threadIdx.x / LPC;
-    const int n0 = q * 4;
-    const bool live = e < a.E && n0 < a.N;
-    const int g = e < a.E ? e / (a.E / a.G) : 0;
-    float A2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float Dv = 0.0f, bias = 0.0f;
-    if (live) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + (size_t)e * a.N + n0));
-        A2[0] = v.x * kLog2e; A2[1] = v.y * kLog2e; A2[2] = v.z * kLog2e; A2[3] = v.w * kLog2e;
-    }
-    if (e < a.E) {
-        Dv = a.D ? a.D[e] : 0.0f;
-        bias = a.dt_bias ? a.dt_bias[e] : 0.0f;
-    }
+    constexpr int CH = kUpdThreads / LPC, NP = 4 * LPC;
+    __shared__ float2 dx[ROWS][CH];                   // dt, x = dt u; y takes dt's place
+    __shared__ float4 Bs[ROWS][LPC], Cs[ROWS][LPC];
+    const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC;
+    const int per_group = a.E / a.G, tiles = (per_group + CH - 1) / CH;
+    const int g = blockIdx.y / tiles;
+    const int e0 = g * per_group + (blockIdx.y - g * tiles) * CH;
+    const int e_end = min(e0 + CH, (g + 1) * per_group);
+    const int e = e0 + cl, n0 = q * 4;
+    const bool live = e < e_end && n0 < a.N;
     const Slots sl{a.sl.cu, a.sl.seq_of, a.sl.slot_of, a.sl.init_slot, a.sl.nseq, a.sl.nslots, a.sl.block, a.sl.status};
     const int64_t slot_elems = (int64_t)a.E * a.N;
     const int64_t off = (int64_t)e * a.N + n0;
@@ -72,35 +70,69 @@ __global__ void __launch_bounds__(kUpdThreads) diag_update_kernel(const DiagArgs
         if (live && to[k] >= 0 && from[k] >= 0)
             st[k] = __ldcs(reinterpret_cast<const float4*>(a.init + from[k] * slot_elems + off));
     }
+
+    // rows left out are staged too: their inputs exist (i < rows) and nothing of them is kept
+    for (int k = tid; k < ROWS * CH; k += kUpdThreads) {
+        const int row = k / CH, c = k % CH;
+        const int64_t i = i0 + row;
+        float2 v = make_float2(0.0f, 0.0f);
+        if (i < a.rows && e0 + c < e_end) {
+            v.x = softplus_series(ld_f(static_cast<const T*>(a.dt) + i * a.dts + e0 + c) + (a.dt_bias ? a.dt_bias[e0 + c] : 0.0f));
+            v.y = v.x * ld_f(static_cast<const T*>(a.u) + i * a.us + e0 + c);
+        }
+        dx[row][c] = v;
+    }
+    for (int k = tid; k < ROWS * NP; k += kUpdThreads) {
+        const int row = k / NP, n = k % NP;
+        const int64_t i = i0 + row;
+        const bool ok = i < a.rows && n < a.N;
+        reinterpret_cast<float*>(Bs)[k] = ok ? ld_f(static_cast<const T*>(a.B) + i * a.bcs + g * a.N + n) : 0.0f;
+        reinterpret_cast<float*>(Cs)[k] = ok ? ld_f(static_cast<const T*>(a.C) + i * a.bcs + g * a.N + n) : 0.0f;
+    }
+    float A2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (live) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + off));
+        A2[0] = v.x * kLog2e; A2[1] = v.y * kLog2e; A2[2] = v.z * kLog2e; A2[3] = v.w * kLog2e;
+    }
+    __syncthreads();
+
+    float acc[ROWS];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-        if (to[k] < 0) continue;
-        const int64_t i = i0 + k;
+        const float2 d = dx[k][cl];
+        const float4 b = Bs[k][q], c = Cs[k][q];
         float4 h = st[k];
-        float acc = 0.0f, uv = 0.0f;
-        if (live) {
-            uv = ld_f(static_cast<const T*>(a.u) + i * a.us + e);
-            const float dt = softplus_series(ld_f(static_cast<const T*>(a.dt) + i * a.dts + e) + bias);
-            const float x = dt * uv;
-            const T* Bp = static_cast<const T*>(a.B) + i * a.bcs + g * a.N + n0;
-            const T* Cp = static_cast<const T*>(a.C) + i * a.bcs + g * a.N + n0;
-            h.x = fmaf(ex2(dt * A2[0]), h.x, x * ld_f(Bp + 0));
-            h.y = fmaf(ex2(dt * A2[1]), h.y, x * ld_f(Bp + 1));
-            h.z = fmaf(ex2(dt * A2[2]), h.z, x * ld_f(Bp + 2));
-            h.w = fmaf(ex2(dt * A2[3]), h.w, x * ld_f(Bp + 3));
-            acc = fmaf(h.x, ld_f(Cp + 0), fmaf(h.y, ld_f(Cp + 1), fmaf(h.z, ld_f(Cp + 2), h.w * ld_f(Cp + 3))));
-            __stcs(reinterpret_cast<float4*>(a.final_state + to[k] * slot_elems + off), h);
-        }
+        h.x = fmaf(ex2(d.x * A2[0]), h.x, d.y * b.x);
+        h.y = fmaf(ex2(d.x * A2[1]), h.y, d.y * b.y);
+        h.z = fmaf(ex2(d.x * A2[2]), h.z, d.y * b.z);
+        h.w = fmaf(ex2(d.x * A2[3]), h.w, d.y * b.w);
+        acc[k] = fmaf(h.x, c.x, fmaf(h.y, c.y, fmaf(h.z, c.z, h.w * c.w)));
+        if (live && to[k] >= 0) __stcs(reinterpret_cast<float4*>(a.final_state + to[k] * slot_elems + off), h);
+    }
+    int at = 0;
+    scatter_sum<ROWS, LPC, 1>(acc, q, at);
+    constexpr int KEPT = LPC < ROWS ? ROWS / LPC : 1;
 #pragma unroll
-        for (int o = LPC / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-        if (q == 0 && e < a.E) {
-            float y = fmaf(Dv, uv, acc);
-            if (a.z) {
-                const float zv = ld_f(static_cast<const T*>(a.z) + i * a.zs + e);
-                y *= zv * sigmoid_f(zv);
-            }
-            static_cast<T*>(a.y)[i * a.E + e] = io<T>::from_f(y);
+    for (int k = 0; k < KEPT; ++k) dx[at + k][cl].x = acc[k];
+    __syncthreads();
+    for (int k = tid; k < ROWS * CH; k += kUpdThreads) {
+        const int row = k / CH, c = k % CH;
+        const int64_t i = i0 + row;
+        bool out = i < a.rows && e0 + c < e_end;
+        if (out && sl.cu) {
+            // as above, by row
+            const int r = sl.seq_of[i];
+            out = r >= 0 && r < sl.nseq && sl.cu[r] == i && sl.cu[r + 1] == i + 1 && sl.init_slot[r] < sl.nslots &&
+                  slot_at(sl, sl.slot_of[i]) >= 0;
         }
+        if (!out) continue;
+        float y = dx[row][c].x;
+        if (a.D) y = fmaf(a.D[e0 + c], ld_f(static_cast<const T*>(a.u) + i * a.us + e0 + c), y);
+        if (a.z) {
+            const float zv = ld_f(static_cast<const T*>(a.z) + i * a.zs + e0 + c);
+            y *= zv * sigmoid_f(zv);
+        }
+        static_cast<T*>(a.y)[i * a.E + e0 + c] = io<T>::from_f(y);
     }
 }
 
@@ -108,7 +140,7 @@ template <typename T, int LPC>
 cudaError_t launch_lpc(const DiagArgs& a, cudaStream_t s)
 {
     constexpr int CH = kUpdThreads / LPC;
-    const int tiles = (a.E + CH - 1) / CH;
+    const int tiles = (a.E / a.G + CH - 1) / CH * a.G;
     const dim3 grid((unsigned)((a.rows + kUpdRows - 1) / kUpdRows), (unsigned)tiles);
     diag_update_kernel<T, LPC, kUpdRows><<<grid, kUpdThreads, 0, s>>>(a);
     return cudaGetLastError();

@@ -46,27 +46,25 @@ class StateMap(NamedTuple):
 class _On:
     """The device and stream of a call: the tensors' device is made current
     for it, and what the call allocates is tied to `stream` where that is not
-    the current one."""
+    the current one.  (The current stream is asked for by its raw handle: a
+    Stream object would cost as much host time as the launch.)"""
+    __slots__ = ("device", "handle", "other", "switch", "scratch", "unread")
 
     def __init__(self, like: torch.Tensor, stream):
         if not like.is_cuda:
             raise ValueError("CUDA tensors expected")
         self.device = like.device
-        self.given = stream
-        self.switch = None
+        index = like.get_device()
+        if stream is not None and stream.device != self.device:
+            raise ValueError("stream and tensors are on different devices")
+        self.switch = None if index == torch.cuda.current_device() else torch.cuda.device(self.device)
+        now = torch._C._cuda_getCurrentRawStream(index)
+        self.handle = now if stream is None else stream.cuda_stream
+        self.other = stream if self.handle != now else None
 
     def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.switch = torch.cuda.device(self.device)
+        if self.switch is not None:
             self.switch.__enter__()
-        s = torch.cuda.current_stream() if self.given is None else self.given
-        if self.given is not None and s.device != self.device:
-            if self.switch is not None:
-                self.switch.__exit__(None, None, None)
-            raise ValueError("stream and tensors are on different devices")
-        self.other = self.given is not None and s != torch.cuda.current_stream()
-        self.stream = s
-        self.handle = s.cuda_stream
         return self
 
     def __exit__(self, *exc):
@@ -75,8 +73,8 @@ class _On:
 
     def empty(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other:
-            t.record_stream(self.stream)
+        if self.other is not None:
+            t.record_stream(self.other)
         return t
 
     def workspace(self, given, need: int):
@@ -84,24 +82,17 @@ class _On:
         if given is None:
             if not need:
                 return None, 0
-            given = self.empty(need, torch.uint8)
-            self.kept = given
-        _on_device(given, "workspace", self.device)
-        if not given.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+            given = self.scratch = self.empty(need, torch.uint8)
+        elif given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
         return given.data_ptr(), given.numel() * given.element_size()
 
 
-def _on_device(t, name, device):
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-
-
 def _dense(t, name, dtype, shape, device):
-    """A contiguous tensor of this type and shape (None passes)."""
+    """The pointer of a contiguous tensor of this type and shape (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
@@ -111,35 +102,43 @@ def _rows(t, name, lead, E, like) -> tuple[int | None, int]:
     spaced and dense."""
     if t is None:
         return None, E
-    if tuple(t.shape) != (*lead, E) or t.dtype != like.dtype or t.device != like.device:
+    if t.shape != (*lead, E) or t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} must be a {like.dtype} tensor of shape {(*lead, E)} on {like.device}")
-    st = t.stride()
-    rows = 1
-    for k in lead:
-        rows *= k
-    if rows == 0:
-        return None, E
-    if st[-1] != 1 or (len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]):
-        raise ValueError(f"{name} must have dense, evenly spaced rows")
+    return t.data_ptr(), _row_stride(t, t.stride(), name, lead, E)
+
+
+def _row_stride(t, st, name, lead, E) -> int:
     # a dimension of one row says nothing about the spacing
-    rs = st[-2] if lead[-1] > 1 else (st[0] if len(lead) == 2 and lead[0] > 1 else E)
-    return t.data_ptr(), rs
+    L = lead[-1]
+    if st[-1] != 1 and E > 1 and t.numel():
+        raise ValueError(f"{name} must have dense rows")
+    if len(lead) == 1:
+        return st[0] if L > 1 else E
+    if not t.numel():
+        return E
+    if lead[0] > 1 and L > 1 and st[0] != L * st[1]:
+        raise ValueError(f"{name} must have evenly spaced rows")
+    return st[1] if L > 1 else st[0] if lead[0] > 1 else E
 
 
 def _bc(B, C, lead, like) -> tuple[int | None, int | None, int, int, int]:
     """B, C [*lead, G, N] as (pointer, pointer, row stride, G, N)."""
-    if B.dim() != len(lead) + 2 or B.shape != C.shape:
-        raise ValueError("B and C must share the shape [.., G, N]")
-    G, N = B.shape[-2], B.shape[-1]
-    out = []
+    shape = B.shape
+    if shape != C.shape or len(shape) != len(lead) + 2 or shape[:-2] != lead:
+        raise ValueError(f"B and C must share the shape {(*lead, 'G', 'N')}")
+    G, N = shape[-2], shape[-1]
+    rs = None
     for t, name in ((B, "B"), (C, "C")):
-        if N > 1 and t.stride(-1) != 1 or G > 1 and t.stride(-2) != N:
+        if t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
+        st = t.stride()
+        if G > 1 and st[-2] != N and t.numel():
             raise ValueError(f"{name}: dense (G, N) rows expected")
-        out.append(_rows(t.flatten(-2) if t.numel() else t.reshape(*lead, G * N), name, lead, G * N, like))
-    (pB, sB), (pC, sC) = out
-    if sB != sC:
-        raise ValueError("B and C must share one row stride")
-    return pB, pC, sB, G, N
+        s = _row_stride(t, (*st[:-2], st[-1]), name, lead, G * N)
+        if rs is not None and s != rs:
+            raise ValueError("B and C must share one row stride")
+        rs = s
+    return B.data_ptr(), C.data_ptr(), rs, G, N
 
 
 def _map(m: StateMap, T: int, device):
@@ -151,10 +150,8 @@ def _map(m: StateMap, T: int, device):
 
 def _status(status, on):
     if status is None:
-        status = on.empty(1, torch.int32)
-        with torch.cuda.stream(on.stream):
-            status.zero_()
-        on.kept_status = status
+        # of the call's own: nobody reads it, but the kernels need the place
+        status = on.unread = on.empty(1, torch.int32)
     return _dense(status, "status", torch.int32, (1,), on.device)
 
 
@@ -178,8 +175,11 @@ def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_l
     with _On(lens, stream) as on:
         dev = on.device
         if out is None:
-            out = StateMap(on.empty(n + 1, i32), on.empty(T, i32), on.empty(T, i32), on.empty(T, torch.int64), on.empty(n, i32),
-                           on.empty((n, mb), i32), on.empty(1, i32), block_tokens)
+            # one allocation for the int32 parts; seq_of and pos_of on 16 bytes
+            n4, T4 = (n + 4) // 4 * 4, (T + 3) // 4 * 4
+            cu, _, seq, _, pos, _, init, _, tab, head = on.empty(n4 + 2 * T4 + n4 + n * mb + 1, i32).split_with_sizes(
+                (n + 1, n4 - n - 1, T, T4 - T, T, T4 - T, n, n4 - n, n * mb, 1))
+            out = StateMap(cu, seq, pos, on.empty(T, torch.int64), init, tab.view(n, mb), head, block_tokens)
         cu, seq, slot, init, _ = _map(out, T, dev)
         pos = _dense(out.pos_of, "pos_of", i32, (T,), dev)
         wp, wb = on.workspace(workspace, int(libssd.ssd_state_map_workspace_bytes(n)))
