@@ -57,6 +57,25 @@ __device__ inline float softplus_series(float v)
     return fmaxf(v, 0.0f) + (w + w) * p;
 }
 
+// The same on a pair, in packed arithmetic, with e = 2^(-|v| log2 e) from the
+// hardware exponential (its argument's rounding adds |v| 2^-24 to e's
+// relative error).
+__device__ inline float2 softplus_pair(float2 v)
+{
+    const float2 e = make_float2(ex2(fabsf(v.x) * -kLog2e), ex2(fabsf(v.y) * -kLog2e));
+    // (one reciprocal for both would let a NaN of one row into the other)
+    const float2 w = make_float2(__fdividef(e.x, 2.0f + e.x), __fdividef(e.y, 2.0f + e.y));
+    const float2 q = pk_mul(w, w);
+    auto both = [](float c) { return make_float2(c, c); };
+    float2 p = pk_fma(q, both(1.0f / 13.0f), both(1.0f / 11.0f));
+    p = pk_fma(q, p, both(1.0f / 9.0f));
+    p = pk_fma(q, p, both(1.0f / 7.0f));
+    p = pk_fma(q, p, both(1.0f / 5.0f));
+    p = pk_fma(q, p, both(1.0f / 3.0f));
+    p = pk_fma(q, p, both(1.0f));
+    return pk_fma(pk_mul(w, both(2.0f)), p, make_float2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+}
+
 // 1 / (1 + e^-v)
 __device__ inline float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
@@ -115,6 +134,24 @@ template <typename T> struct Raw8 {
         }
     }
 };
+
+// 4 adjacent elements of any alignment; `vec`: they are aligned to their size.
+template <typename T> __device__ inline void load4(const T* p, bool vec, float (&v)[4])
+{
+    if (vec) {
+        if constexpr (sizeof(T) == 2) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+            v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+            v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+        } else {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ld_f(p + i);
+    }
+}
 
 // A packed batch's requests and state slots (device pointers; see ssd_diag.h).
 struct Slots {
@@ -204,12 +241,13 @@ __device__ inline bool find_piece_packed(int q, const Slots& sl, int rows, int s
         if (at - p.s0 <= keep) return false;
         p.t0 = (int)at;
     }
-    int64_t cut = ((int64_t)p.t0 / seg + 1) * seg;
-    if (p.t0 == p.s0 && cut - p.s0 <= keep) cut += seg;
+    int64_t second = ((int64_t)p.s0 / seg + 1) * seg;   // where the sequence's second piece starts
+    if (second - p.s0 <= keep) second += seg;           // (keep < seg)
+    const int64_t cut = p.t0 == p.s0 ? second : (int64_t)p.t0 + seg;
     p.t1 = (int)(cut < p.s1 ? cut : p.s1);
     p.idx = q;
     p.first = p.r;
-    p.next = sl.nseq + p.s0 / seg;
+    p.next = sl.nseq + second / seg - 1;
     return true;
 }
 

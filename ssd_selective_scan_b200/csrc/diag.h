@@ -51,24 +51,32 @@ struct DiagArgs {
     bool bf16;
     SlotArgs sl;
     void* ws;
-    float* ckpt = nullptr;
+    // for the backward pass (launch_diag_ckpt)
+    const void* dy = nullptr;
+    float *ckpt = nullptr, *gl = nullptr, *gsdt = nullptr;
+    int bseg = 0;
+    bool longest_first = false;   // packed: sequences are taken up by length
+    bool bc_aligned = false;   // every 4 elements of a B or C row are aligned to their size
 };
 size_t diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G);
 cudaError_t launch_diag_scan(const DiagArgs& a, cudaStream_t s);
 cudaError_t launch_diag_update(const DiagArgs& a, cudaStream_t s);
 
-// The states before every kDiagCkpt-th row of each sequence, for the backward
-// pass, to a.ckpt [nseq][ckpts_of(L)][E][N]; rows cut every seg rows (a
-// multiple of kDiagCkpt; L or more: not at all).  A cut walk leaves every
-// piece's final state and sum of dt in a.ws, diag_cut_bytes(...) bytes: [piece]
-// [E][N], then [piece][E], then the sequences' initial states.
+// What the backward pass starts from.  The states before every kDiagCkpt-th
+// row of each sequence, to a.ckpt [nseq][ckpts_of(L)][E][N].  Where it walks
+// the rows in pieces of a.bseg < L (a multiple of 32): for each piece [nseq]
+// [pieces] the part of the state gradient at its start that comes from its
+// own rows, to a.gl [E][N], and the sum of its dt, to a.gsdt [E].  The walk is
+// itself cut every diag_ckpt_rows(...) rows (L: not at all), with
+// diag_cut_bytes(...) of workspace at a.ws.
 constexpr int kDiagCkpt = 8;
 #ifdef __CUDACC__
 __host__ __device__
 #endif
 inline int64_t ckpts_of(int L) { return ((int64_t)L + kDiagCkpt - 1) / kDiagCkpt; }
+int diag_ckpt_rows(int b, int L, int E, int N, int G, int bseg);
 size_t diag_cut_bytes(int nseq, int64_t pieces, int E, int N);
-cudaError_t launch_diag_ckpt(const DiagArgs& a, int seg, cudaStream_t s);
+cudaError_t launch_diag_ckpt(const DiagArgs& a, cudaStream_t s);
 
 struct DiagBwdArgs {
     DiagArgs f;            // the forward call's inputs

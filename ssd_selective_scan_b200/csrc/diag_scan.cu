@@ -10,17 +10,23 @@
 // special-function unit (16 results per cycle and SM: N = 16 states cost a
 // cycle per token and channel), before HBM (8 bytes per token and channel).
 //
-// Layout.  LPC lanes share a channel, 4 states each, so a CTA of 128 threads
-// covers CH = 128 / LPC channels of one group.  It walks the tokens of a
-// piece of a sequence in tiles of TT: u, dt_raw and z come in 16-byte vectors
-// while the tile before is computed, dt = softplus(dt_raw + bias) and
-// x = dt u are formed once per (token, channel) by the thread that loaded
-// them and handed to the channel's lanes through shared memory, as are the
-// tile's B and C rows.  The state stays in registers for the whole piece.
-// y's sum over the states is finished 4 tokens at a time: each step of the
-// exchange halves the tokens a lane keeps, so 4 lanes need 3 shuffles for 4
-// tokens.  y goes back through shared memory to the loading threads, which
-// add D u, gate and store 16-byte vectors.
+// Layout.  A CTA covers CH channels of one group (diag_tile.cuh) and walks
+// the tokens of a piece of a sequence in tiles of TT.  Two warps hold the
+// states and run the recurrence; two more feed them, taking turns at the
+// tiles: they copy u, dt_raw and z to shared memory ahead (cp.async), form dt
+// = softplus(dt_raw + bias) and x = dt u once per (token, channel), lay them
+// out with the tile's B and C rows, and finish the tile before: add D u to
+// the sums over the states, gate, store 16-byte vectors.  Done by the same
+// warps in turn these steps added their latencies to the recurrence's.  The
+// sides meet at named barriers, a pair for each of the two tile buffers; a
+// feeding warp has its next tile ready in registers when the buffer comes
+// free.
+//
+// Rows lie in pairs, as the packed fp32 instructions take them: dt of rows 2i
+// and 2i + 1 side by side, and so x, B and C.  exp, x B and the sum with C
+// then work on both rows at once with no register copied; only the two steps
+// of h itself are scalar.  y's sum over the states is finished 4 tokens at a
+// time, each lane ending with two of them.
 //
 // Few rows.  A lane's tokens are a serial chain, and a narrow layer's single
 // prompt has too few lanes to fill the device.  The rows are then cut into
@@ -31,29 +37,54 @@
 // second kernel computes at its start before it walks the piece for y.  The
 // exponentials are paid twice, so the rows are cut only where the lanes of
 // one sequence leave the device idle (piece_rows).
-#include "diag.cuh"
-#include "diag.h"
+#include <type_traits>
+
+#include "diag_tile.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 2;                  // of each kind
+constexpr int kThreads = 2 * 32 * kWarps;
 
-template <int LPC> struct Tile {
-    static constexpr int CH = kThreads / LPC;             // channels per CTA
-    static constexpr int TT = LPC < 4 ? 8 * LPC : 32;     // tokens per tile
-    static constexpr int NP = 4 * LPC;                    // states, padded
-    static constexpr int VPR = CH / 8;                    // 8-element vectors per row
-    static constexpr int NVEC = TT * VPR;                 // ... per tile: at most one per thread
-    static constexpr int PAD = CH + 1;                    // float2 per row of the dt | x tile
-    static_assert(NVEC <= kThreads, "one vector per thread");
+// What a walk leaves: a piece's final state and sum of dt (in the workspace),
+// y and the states, or what the backward pass starts from: the states every
+// kDiagCkpt rows and, where it walks the rows in pieces, each piece's part of
+// the state gradient at its start.
+enum Mode { kLocal, kOutput, kCkpt, kCkptG };
+
+template <typename T, int LPC, Mode MODE> struct Smem {
+    using TL = DiagTile<LPC, kWarps>;
+    static constexpr int NT = MODE == kCkptG ? 4 : MODE == kOutput ? 3 : 2;
+    static constexpr int PAIRS = TL::TT / 2;
+    float4 dx[2][PAIRS][TL::CH];                     // dt, dt', x, x' of two rows
+    float4 B[2][PAIRS][LPC][2], C[2][PAIRS][LPC][2]; // b0, b0', b1, b1', b2, ..
+    float2 p[MODE == kCkptG ? 2 : 1][MODE == kCkptG ? PAIRS : 1][TL::CH];   // dy SiLU(z)
+    T raw[kWarps][3][NT][TL::TT][TL::CH];            // u, dt_raw, z, dy
 };
 
-template <int LPC> struct Smem {
-    float2 dx[2][Tile<LPC>::TT * Tile<LPC>::PAD];   // dt, x = dt u; y takes dt's place
-    float4 B[2][Tile<LPC>::TT * LPC];
-    float4 C[2][Tile<LPC>::TT * LPC];
-};
+// Packed sequences that a CTA ranks by length: one per thread, and only where
+// they are long enough for a few hundred comparisons not to matter.
+constexpr int kSortSeqs = kThreads;
+constexpr int kSortRows = 128;   // rows per sequence
+
+constexpr int kMeeting = 32 * (kWarps + 1);   // a feeding warp and the walking ones
+
+// Named barriers of the two tile buffers: laid out, and walked.  The numbers
+// are literals: a barrier number in a register makes the CTA hold all 16, and
+// an SM then holds 4 CTAs at most.
+template <int FIRST> __device__ inline void bar_sync(int buf)
+{
+    if (buf) asm volatile("bar.sync %0, %1;" ::"n"(FIRST + 1), "n"(kMeeting) : "memory");
+    else asm volatile("bar.sync %0, %1;" ::"n"(FIRST), "n"(kMeeting) : "memory");
+}
+template <int FIRST> __device__ inline void bar_arrive(int buf)
+{
+    if (buf) asm volatile("bar.arrive %0, %1;" ::"n"(FIRST + 1), "n"(kMeeting) : "memory");
+    else asm volatile("bar.arrive %0, %1;" ::"n"(FIRST), "n"(kMeeting) : "memory");
+}
+constexpr int kFull = 1, kDone = 3;
+
 
 // Workspace of a cut scan: per piece its final state and sum of dt, and the
 // initial state of every sequence (a piece that runs later may write the
@@ -71,44 +102,41 @@ __host__ __device__ inline CutWs cut_ws(void* ws, int64_t pieces, int E, int N)
 }
 inline size_t cut_ws_bytes(int nseq, int64_t pieces, int E, int N) { return ((size_t)pieces * E * (N + 1) + (size_t)nseq * E * N) * 4; }
 
-// What a walk leaves: a piece's final state and sum of dt (in the workspace),
-// y and the states, or the states every kDiagCkpt rows.
-enum Mode { kLocal, kOutput, kCkpt };
-
 // CUT: the pieces' states are in the workspace.
 template <typename T, int LPC, bool PACKED, Mode MODE, bool CUT>
-__global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, int seg, int64_t pieces)
+__global__ void __launch_bounds__(kThreads, MODE == kOutput && sizeof(T) == 2 ? 5 : 4) diag_scan_kernel(const DiagArgs a, int seg, int64_t pieces)
 {
-    constexpr bool FULL = MODE == kOutput;
-    using TL = Tile<LPC>;
-    constexpr int CH = TL::CH, TT = TL::TT, VPR = TL::VPR, PAD = TL::PAD;
+    using TL = DiagTile<LPC, kWarps>;
+    constexpr bool OUT = MODE == kOutput, WITH_C = OUT || MODE == kCkptG;
+    constexpr int TT = TL::TT, PAIRS = TT / 2, VPR = TL::VPR;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<LPC>& sm = *reinterpret_cast<Smem<LPC>*>(smem_raw);
+    Smem<T, LPC, MODE>& sm = *reinterpret_cast<Smem<T, LPC, MODE>*>(smem_raw);
 
     const Slots sl{a.sl.cu, a.sl.seq_of, a.sl.slot_of, a.sl.init_slot, a.sl.nseq, a.sl.nslots, a.sl.block, a.sl.status};
     Piece p;
-    if (!(PACKED ? find_piece_packed(blockIdx.x, sl, a.rows, seg, 0, p) : find_piece_dense(blockIdx.x, a.L, seg, p))) return;
+    const int ntiles = channel_tiles(a.E, a.G, TL::CH) * a.G;
+    const int piece = (int)(blockIdx.x / ntiles);   // a piece's CTAs start together
+    int which = piece;
+    if constexpr (PACKED) {
+        // longest sequences first, or the last ones to start are walked alone
+        __shared__ int lens[kSortSeqs], chosen;
+        if (a.longest_first && piece < a.nseq) {
+            const int me = threadIdx.x;
+            lens[me] = me < a.nseq ? sl.cu[me + 1] - sl.cu[me] : -1;
+            __syncthreads();
+            int rank = 0;
+            for (int i = 0; i < a.nseq; ++i) rank += lens[i] > lens[me] || (lens[i] == lens[me] && i < me);
+            if (me < a.nseq && rank == piece) chosen = me;
+            __syncthreads();
+            which = chosen;
+        }
+    }
+    if (!(PACKED ? find_piece_packed(which, sl, a.rows, seg, seg - 1, p) : find_piece_dense(which, a.L, seg, p))) return;
     if (MODE == kLocal && p.t1 == p.s1) return;   // no successor
 
-    const int tid = threadIdx.x;
-    const int q = tid % LPC, cl = tid / LPC;
-    const int per_group = a.E / a.G, tiles = (per_group + CH - 1) / CH;
-    const int g = blockIdx.y / tiles;
-    const int e0 = g * per_group + (blockIdx.y - g * tiles) * CH;     // the CTA's first channel
-    const int e_end = min(e0 + CH, (g + 1) * per_group);
-    const int e = e0 + cl, n0 = 4 * q;
-    const bool live = e < e_end && n0 < a.N;
-    const int64_t st = (int64_t)e * a.N + n0;
-    const int64_t st_all = (int64_t)a.E * a.N;
-
-    float A2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + st));
-        A2[0] = v.x * kLog2e; A2[1] = v.y * kLog2e; A2[2] = v.z * kLog2e; A2[3] = v.w * kLog2e;
-    }
-
-    // the piece's initial state
-    int init_at = -1;
+    const ChannelTile ct(a.E, a.G, TL::CH, blockIdx.x - piece * ntiles);
+    const int e0 = ct.e0, e_end = ct.e_end;
+    int init_at = -1;   // where the sequence's initial state is
     if constexpr (PACKED) {
         init_at = sl.init_slot[p.r];
         if (init_at >= sl.nslots) {
@@ -118,219 +146,389 @@ __global__ void __launch_bounds__(kThreads) diag_scan_kernel(const DiagArgs a, i
     } else {
         init_at = a.init ? p.r : -1;
     }
-    float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto load_h = [&](const float* src) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
-    };
-    auto store_h = [&](float* dst) { *reinterpret_cast<float4*>(dst) = make_float4(h[0], h[1], h[2], h[3]); };
-    const CutWs ws = cut_ws(a.ws, pieces, a.E, a.N);
-    const bool head = p.t0 == p.s0;
-    if (live) {
-        if (!CUT || (head && (MODE == kLocal || p.t1 == p.s1))) {
-            if (head && init_at >= 0) load_h(a.init + init_at * st_all + st);
-            if (CUT && MODE == kLocal && head) store_h(ws.h0 + p.r * st_all + st);
-        } else if (head) {
-            load_h(ws.h0 + p.r * st_all + st);
-        } else if (MODE != kLocal) {
-            load_h(ws.h + p.first * st_all + st);
-            for (int64_t i = p.next; i < p.idx; ++i) {
-                const float sdt = ws.sdt[i * a.E + e];
-                const float4 v = *reinterpret_cast<const float4*>(ws.h + i * st_all + st);
-                h[0] = fmaf(ex2(A2[0] * sdt), h[0], v.x);
-                h[1] = fmaf(ex2(A2[1] * sdt), h[1], v.y);
-                h[2] = fmaf(ex2(A2[2] * sdt), h[2], v.z);
-                h[3] = fmaf(ex2(A2[3] * sdt), h[3], v.w);
+    const int ntile = (p.t1 - p.t0 + TT - 1) / TT;
+    // y's sums over the states, of the last 4 tiles
+    __shared__ float2 ys[4][OUT ? PAIRS : 1][TL::CH];
+
+    // The walking warps are the ones that need the special-function units, of
+    // which each of the SM's four partitions has one; a warp runs on the
+    // partition of its place on the SM modulo 4.  So which half of the CTA
+    // walks goes by the CTA's place: neighbours take different halves.
+    // (Wherever the places are, either half does the work.)
+    __shared__ uint32_t place;
+    if (threadIdx.x == 0) asm volatile("mov.u32 %0, %%warpid;" : "=r"(place));
+    __syncthreads();
+    const int me = (int)(threadIdx.x ^ ((place >> 2 & 1) * (32 * kWarps)));
+    if (me >= 32 * kWarps) {
+        // ---- the feeding warps, one to a buffer: rows 2 pr and 2 pr + 1, vector sv
+        const int fl = me & 31, buf = (me >> 5) - kWarps;
+        const int pr = fl / VPR, sv = fl % VPR;
+        const int ev = e0 + 8 * sv;
+        const bool copies = fl < PAIRS * VPR && ev < e_end;
+        auto& raws = sm.raw[buf];
+        const T* up = static_cast<const T*>(a.u) + ev;
+        const T* dp = static_cast<const T*>(a.dt) + ev;
+        const T* zp = static_cast<const T*>(a.z) + ev;
+        const T* gp = static_cast<const T*>(a.dy) + ev;
+        auto fetch = [&](int i) {        // tile i, on its way
+            if (i < ntile && copies) {
+                auto& raw = raws[(i >> 1) % 3];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int64_t row = p.t0 + i * TT + 2 * pr + k;
+                    if (row >= p.t1) break;
+                    cp_row8(&raw[0][2 * pr + k][8 * sv], up + row * a.us);
+                    cp_row8(&raw[1][2 * pr + k][8 * sv], dp + row * a.dts);
+                    if (WITH_C && a.z) cp_row8(&raw[2 * WITH_C][2 * pr + k][8 * sv], zp + row * a.zs);
+                    if (MODE == kCkptG) cp_row8(&raw[MODE == kCkptG ? 3 : 0][2 * pr + k][8 * sv], gp + row * a.E);
+                }
             }
-        }
-    }
-
-    // staging: vector sv of row sr of each tile
-    const int sr = tid / VPR, sv = tid % VPR;
-    const bool stages = tid < TL::NVEC && e0 + 8 * sv < e_end;
-    float Dv[8], bias[8];
+            cp_commit();
+        };
+        // B and C: pair of rows bp, states 4 bq .. of this thread's items
+        constexpr int ITEMS = (PAIRS * LPC + 31) / 32;
+        const T* Bp = static_cast<const T*>(a.B) + (int64_t)ct.group * a.N;
+        const T* Cp = static_cast<const T*>(a.C) + (int64_t)ct.group * a.N;
+        const bool vec = a.bc_aligned;
+        float bv[ITEMS][2][4], cv[ITEMS][2][4];
+        auto fetch_bc = [&](int i) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        Dv[j] = FULL && stages && a.D ? a.D[e0 + 8 * sv + j] : 0.0f;
-        bias[j] = stages && a.dt_bias ? a.dt_bias[e0 + 8 * sv + j] : 0.0f;
-    }
-    const T* up = static_cast<const T*>(a.u) + e0 + 8 * sv;
-    const T* dp = static_cast<const T*>(a.dt) + e0 + 8 * sv;
-    const T* zp = static_cast<const T*>(a.z) + e0 + 8 * sv;
-    T* yp = static_cast<T*>(a.y) + e0 + 8 * sv;
-    const T* Bp = static_cast<const T*>(a.B) + (int64_t)g * a.N;
-    const T* Cp = static_cast<const T*>(a.C) + (int64_t)g * a.N;
-
-    Raw8<T> u_now, z_now, u_next, z_next, dt_next;
-    constexpr int NBC = (TT * TL::NP + kThreads - 1) / kThreads;   // B (and C) elements per thread and tile
-    float b_next[NBC], c_next[NBC];
-    auto fetch = [&](int t) {   // the tile that starts at row t: into registers
-        u_next.zero();
-        z_next.zero();
-        if (stages && t + sr < p.t1) {
-            u_next.load(up + (int64_t)(t + sr) * a.us);
-            dt_next.load(dp + (int64_t)(t + sr) * a.dts);
-            if (FULL && a.z) z_next.load(zp + (int64_t)(t + sr) * a.zs);
-        }
+            for (int k = 0; k < ITEMS; ++k) {
+                const int at = fl + 32 * k, bp = at / LPC, bq = at % LPC;
 #pragma unroll
-        for (int i = 0; i < NBC; ++i) {
-            const int k = tid + i * kThreads;
-            const int row = k / TL::NP, n = k % TL::NP;
-            const bool ok = k < TT * TL::NP && t + row < p.t1 && n < a.N;
-            b_next[i] = ok ? ld_f(Bp + (int64_t)(t + row) * a.bcs + n) : 0.0f;
-            if (FULL) c_next[i] = ok ? ld_f(Cp + (int64_t)(t + row) * a.bcs + n) : 0.0f;
-        }
-    };
-    auto stage = [&](int t, int buf) {   // registers to shared memory; rows behind the piece change nothing
-        if (tid < TL::NVEC) {
-            const bool ok = stages && t + sr < p.t1;
+                for (int w = 0; w < 2; ++w) {
+                    const int64_t row = p.t0 + i * TT + 2 * bp + w;
+                    const bool ok = at < PAIRS * LPC && row < p.t1 && 4 * bq < a.N;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) bv[k][w][e] = cv[k][w][e] = 0.0f;
+                    if (ok) load4(Bp + row * a.bcs + 4 * bq, vec, bv[k][w]);
+                    if (ok && WITH_C) load4(Cp + row * a.bcs + 4 * bq, vec, cv[k][w]);
+                }
+            }
+        };
+        // dt and x of tile i, in registers; rows behind the piece change nothing
+        float2 dtv[8], xv[8], pv[MODE == kCkptG ? 8 : 1];
+        auto form = [&](int i) {
+            auto& raw = raws[(i >> 1) % 3];
+            const int row = p.t0 + i * TT + 2 * pr;
+            const bool ok0 = copies && row < p.t1, ok1 = copies && row + 1 < p.t1;
+            if (!copies) return;
+            const Raw8<T> u0 = smem_row8(&raw[0][2 * pr][8 * sv]), u1 = smem_row8(&raw[0][2 * pr + 1][8 * sv]);
+            const Raw8<T> v0 = smem_row8(&raw[1][2 * pr][8 * sv]), v1 = smem_row8(&raw[1][2 * pr + 1][8 * sv]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float dt = ok ? softplus_series(dt_next.get(j) + bias[j]) : 0.0f;
-                sm.dx[buf][sr * PAD + 8 * sv + j] = make_float2(dt, ok ? dt * u_next.get(j) : 0.0f);
+                const float bias = a.dt_bias ? __ldg(a.dt_bias + ev + j) : 0.0f;
+                const float2 dt = softplus_pair(make_float2(v0.get(j) + bias, v1.get(j) + bias));
+                dtv[j] = make_float2(ok0 ? dt.x : 0.0f, ok1 ? dt.y : 0.0f);
+                xv[j] = make_float2(ok0 ? dt.x * u0.get(j) : 0.0f, ok1 ? dt.y * u1.get(j) : 0.0f);
             }
-        }
+            if constexpr (MODE == kCkptG) {
+                const Raw8<T> z0 = smem_row8(&raw[2][2 * pr][8 * sv]), z1 = smem_row8(&raw[2][2 * pr + 1][8 * sv]);
+                const Raw8<T> g0 = smem_row8(&raw[3][2 * pr][8 * sv]), g1 = smem_row8(&raw[3][2 * pr + 1][8 * sv]);
 #pragma unroll
-        for (int i = 0; i < NBC; ++i) {
-            const int k = tid + i * kThreads;
-            if (k < TT * TL::NP) {
-                reinterpret_cast<float*>(sm.B[buf])[k] = b_next[i];
-                if (FULL) reinterpret_cast<float*>(sm.C[buf])[k] = c_next[i];
+                for (int j = 0; j < 8; ++j) {
+                    float2 g = make_float2(g0.get(j), g1.get(j));
+                    if (a.z) {
+                        g.x *= z0.get(j) * sigmoid_f(z0.get(j));
+                        g.y *= z1.get(j) * sigmoid_f(z1.get(j));
+                    }
+                    pv[j] = make_float2(ok0 ? g.x : 0.0f, ok1 ? g.y : 0.0f);
+                }
+            }
+        };
+        auto finish = [&](int i) {       // the outputs of tile i
+            if constexpr (OUT) {
+                if (!copies) return;
+                auto& raw = raws[(i >> 1) % 3];
+                float o[2][8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 y = ys[i & 3][pr][TL::col8(8 * sv + j, pr)];
+                    o[0][j] = y.x;
+                    o[1][j] = y.y;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int64_t row = p.t0 + i * TT + 2 * pr + k;
+                    if (row >= p.t1) break;
+                    const Raw8<T> u = smem_row8(&raw[0][2 * pr + k][8 * sv]), z = smem_row8(&raw[2][2 * pr + k][8 * sv]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (a.D) o[k][j] = fmaf(__ldg(a.D + ev + j), u.get(j), o[k][j]);
+                        if (a.z) {
+                            const float zv = z.get(j);
+                            o[k][j] *= zv * sigmoid_f(zv);
+                        }
+                    }
+                    Raw8<T>::store(static_cast<T*>(a.y) + row * a.E + ev, o[k]);
+                }
+            }
+        };
+        fetch(buf);
+        fetch(buf + 2);
+        if (buf < ntile) {
+            fetch_bc(buf);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");   // a thread reads back what it copied itself
+            form(buf);
+        }
+        for (int i = buf; i < ntile; i += 2) {
+            if (i >= 2) bar_sync<kDone>(buf);
+            if (copies) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sm.dx[buf][pr][TL::col16(8 * sv + j, pr)] = make_float4(dtv[j].x, dtv[j].y, xv[j].x, xv[j].y);
+                    if constexpr (MODE == kCkptG) sm.p[buf][pr][TL::col8(8 * sv + j, pr)] = pv[j];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const int at = fl + 32 * k, bp = at / LPC, bq = at % LPC;
+                if (at < PAIRS * LPC) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        sm.B[buf][bp][bq][h] = make_float4(bv[k][0][2 * h], bv[k][1][2 * h], bv[k][0][2 * h + 1], bv[k][1][2 * h + 1]);
+                        if (WITH_C) sm.C[buf][bp][bq][h] = make_float4(cv[k][0][2 * h], cv[k][1][2 * h], cv[k][0][2 * h + 1], cv[k][1][2 * h + 1]);
+                    }
+                }
+            }
+            bar_arrive<kFull>(buf);
+            if (i >= 2) finish(i - 2);
+            fetch(i + 4);
+            if (i + 2 < ntile) {
+                fetch_bc(i + 2);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                form(i + 2);
             }
         }
-    };
+        const int last = ntile - 1 - ((ntile - 1 - buf) & 1);   // this warp's last tile
+        if (last >= 0 && ntile > buf) {
+            bar_sync<kDone>(buf);
+            finish(last);
+        }
+        return;
+    }
+
+    // ---- the walking warps
+    const int lane = me & 31, q = lane % LPC;
+    const int64_t st_all = (int64_t)a.E * a.N;
+    int cl[2];
+    int64_t st[2];
+    bool live[2];
+    float A2[2][4], h[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        cl[j] = TL::channel(me >> 5, lane, j);
+        live[j] = e0 + cl[j] < e_end && 4 * q < a.N;
+        st[j] = (int64_t)(e0 + cl[j]) * a.N + 4 * q;
+        for (int n = 0; n < 4; ++n) A2[j][n] = h[j][n] = 0.0f;
+        if (live[j]) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + st[j]));
+            A2[j][0] = v.x * kLog2e; A2[j][1] = v.y * kLog2e; A2[j][2] = v.z * kLog2e; A2[j][3] = v.w * kLog2e;
+        }
+    }
+    auto put4 = [](float* dst, const float (&v)[4]) { *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]); };
+    const CutWs ws = cut_ws(a.ws, pieces, a.E, a.N);
+    const bool head = p.t0 == p.s0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (!live[j]) continue;
+        auto load_h = [&](const float* src) {
+            const float4 v = *reinterpret_cast<const float4*>(src + st[j]);
+            h[j][0] = v.x; h[j][1] = v.y; h[j][2] = v.z; h[j][3] = v.w;
+        };
+        if (!CUT || (head && (MODE == kLocal || p.t1 == p.s1))) {
+            if (head && init_at >= 0) load_h(a.init + init_at * st_all);
+            if (CUT && MODE == kLocal && head) put4(ws.h0 + p.r * st_all + st[j], h[j]);
+        } else if (head) {
+            load_h(ws.h0 + p.r * st_all);
+        } else if (MODE != kLocal) {
+            load_h(ws.h + p.first * st_all);
+            for (int64_t i = p.next; i < p.idx; ++i) {
+                const float sdt = ws.sdt[i * a.E + e0 + cl[j]];
+                const float4 v = *reinterpret_cast<const float4*>(ws.h + i * st_all + st[j]);
+                h[j][0] = fmaf(ex2(A2[j][0] * sdt), h[j][0], v.x);
+                h[j][1] = fmaf(ex2(A2[j][1] * sdt), h[j][1], v.y);
+                h[j][2] = fmaf(ex2(A2[j][2] * sdt), h[j][2], v.z);
+                h[j][3] = fmaf(ex2(A2[j][3] * sdt), h[j][3], v.w);
+            }
+        }
+    }
 
     // the next row at which a block ends inside the piece (packed)
     int64_t keep = 0x7fffffffffffLL;
-    if (PACKED && FULL) {
+    if (PACKED && OUT) {
         const int64_t flat = sl.slot_of[p.t0];
         if (flat >= 0) keep = (int64_t)p.t0 + sl.block - 1 - flat % sl.block;
     }
     const int keep_end = min(p.t1, p.s1 - 1);   // the sequence's last state is written behind the walk
-    float sdt = 0.0f;
+    float sdt[2] = {0.0f, 0.0f};
+    // the backward pieces' part: P the product of the decays since the
+    // piece's start, Gl = sum_t P_t C_t p_t (of even and odd rows)
+    float P[2][4];
+    float2 Gl[2][4];
+    auto restart = [&] {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            sdt[j] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                P[j][n] = 1.0f;
+                Gl[j][n] = make_float2(0.0f, 0.0f);
+            }
+        }
+    };
+    restart();
 
-    fetch(p.t0);
-    stage(p.t0, 0);
-    u_now = u_next;
-    z_now = z_next;
-    __syncthreads();
-    int buf = 0;
-    for (int t = p.t0; t < p.t1; t += TT, buf ^= 1) {
-        const bool more = t + TT < p.t1;
-        if (more) fetch(t + TT);
-
-        float2* dx = sm.dx[buf];
+    for (int it = 0; it < ntile; ++it) {
+        const int buf = it & 1, t = p.t0 + it * TT;
         const int groups = (min(TT, p.t1 - t) + 3) / 4;
-        for (int gr = 0; gr < groups; ++gr) {
-            if constexpr (MODE == kCkpt) {
+        bar_sync<kFull>(buf);
+        // 4 rows; KEEPS: a block may end in them
+        auto walk4 = [&](int gr, auto keeps) {
+            constexpr bool KEEPS = decltype(keeps)::value;
+            if constexpr (MODE == kCkpt || MODE == kCkptG) {
                 const int row = t + 4 * gr - p.s0;   // pieces start at multiples of kDiagCkpt
-                if (row % kDiagCkpt == 0 && live)
-                    store_h(a.ckpt + ((int64_t)p.r * ckpts_of(a.L) + row / kDiagCkpt) * st_all + st);
-            }
-            float acc[4];
+                if (row % kDiagCkpt == 0)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 4 * gr + i;
-                const float2 d = dx[row * PAD + cl];
-                const float4 b4 = sm.B[buf][row * LPC + q];
-                const float2 dd = make_float2(d.x, d.x), xx = make_float2(d.y, d.y);
-                const float2 e01 = pk_mul(make_float2(A2[0], A2[1]), dd), e23 = pk_mul(make_float2(A2[2], A2[3]), dd);
-                const float2 x01 = pk_mul(make_float2(b4.x, b4.y), xx), x23 = pk_mul(make_float2(b4.z, b4.w), xx);
-                const float2 h01 = pk_fma(make_float2(ex2(e01.x), ex2(e01.y)), make_float2(h[0], h[1]), x01);
-                const float2 h23 = pk_fma(make_float2(ex2(e23.x), ex2(e23.y)), make_float2(h[2], h[3]), x23);
-                h[0] = h01.x; h[1] = h01.y; h[2] = h23.x; h[3] = h23.y;
-                if constexpr (FULL) {
-                    const float4 c4 = sm.C[buf][row * LPC + q];
-                    const float2 y2 = pk_fma(h01, make_float2(c4.x, c4.y), pk_mul(h23, make_float2(c4.z, c4.w)));
-                    acc[i] = y2.x + y2.y;
-                    if (PACKED && t + row == keep) {
-                        // a block ends here: its state to its slot
-                        if (t + row < keep_end) {
-                            const int slot = slot_at(sl, sl.slot_of[t + row]);
-                            if (slot >= 0 && live) store_h(a.final_state + slot * st_all + st);
+                    for (int j = 0; j < 2; ++j)
+                        if (live[j]) put4(a.ckpt + ((int64_t)p.r * ckpts_of(a.L) + row / kDiagCkpt) * st_all + st[j], h[j]);
+            }
+            [[maybe_unused]] float2 acc[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int pr = 2 * gr + i;
+                const float4 bb[2] = {sm.B[buf][pr][q][0], sm.B[buf][pr][q][1]};
+                float4 cc[2];
+                if (WITH_C) cc[0] = sm.C[buf][pr][q][0], cc[1] = sm.C[buf][pr][q][1];
+                float h0[2][4];   // the states after the pair's first row
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float4 d = sm.dx[buf][pr][TL::col16(cl[j], pr)];
+                    const float2 dd = make_float2(d.x, d.y), xx = make_float2(d.z, d.w);
+                    float2 pp;
+                    if constexpr (MODE == kCkptG) pp = sm.p[buf][pr][TL::col8(cl[j], pr)];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float2 b2 = n & 1 ? make_float2(bb[n >> 1].z, bb[n >> 1].w) : make_float2(bb[n >> 1].x, bb[n >> 1].y);
+                        const float2 e = pk_mul(make_float2(A2[j][n], A2[j][n]), dd);
+                        const float a0 = ex2(e.x), a1 = ex2(e.y);
+                        const float2 xb = pk_mul(xx, b2);
+                        h0[j][n] = fmaf(a0, h[j][n], xb.x);
+                        h[j][n] = fmaf(a1, h0[j][n], xb.y);
+                        if constexpr (WITH_C) {
+                            const float2 c2 = n & 1 ? make_float2(cc[n >> 1].z, cc[n >> 1].w) : make_float2(cc[n >> 1].x, cc[n >> 1].y);
+                            if constexpr (OUT) {
+                                const float2 hh = make_float2(h0[j][n], h[j][n]);
+                                acc[j][i] = n ? pk_fma(hh, c2, acc[j][i]) : pk_mul(hh, c2);
+                            } else {
+                                const float P0 = P[j][n] * a0;
+                                P[j][n] = P0 * a1;
+                                Gl[j][n] = pk_fma(make_float2(P0, P[j][n]), pk_mul(c2, pp), Gl[j][n]);
+                            }
                         }
-                        keep += sl.block;
                     }
-                } else if (MODE == kLocal) {
-                    sdt += d.x;
+                    if constexpr (!OUT) sdt[j] += d.x + d.y;
+                }
+                if constexpr (KEEPS) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int row = t + 2 * pr + k;
+                        if (row == keep) {   // a block ends here: its state to its slot
+                            if (row < keep_end) {
+                                const int slot = slot_at(sl, sl.slot_of[row]);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (slot >= 0 && live[j]) put4(a.final_state + slot * st_all + st[j], k ? h[j] : h0[j]);
+                            }
+                            keep += sl.block;
+                        }
+                    }
                 }
             }
-            if constexpr (FULL) {
-                // the channel's lanes join their sums; lane q & 3 ends with token q & 3
-                if constexpr (LPC >= 4) {
-                    const bool hi = q & 2, odd = q & 1;
-                    float k0 = hi ? acc[2] : acc[0], k1 = hi ? acc[3] : acc[1];
-                    const float s0 = hi ? acc[0] : acc[2], s1 = hi ? acc[1] : acc[3];
-                    k0 += __shfl_xor_sync(0xffffffffu, s0, 2);
-                    k1 += __shfl_xor_sync(0xffffffffu, s1, 2);
-                    float k = odd ? k1 : k0;
-                    k += __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
+            if constexpr (OUT) {
+                // slot 0's channel (diag_tile.cuh), then two of the rows
+                float v[4];
 #pragma unroll
-                    for (int o = 4; o < LPC; o <<= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
-                    if (LPC == 4 || q < 4) dx[(4 * gr + (q & 3)) * PAD + cl].x = k;
-                } else if constexpr (LPC == 2) {
-                    const bool odd = q & 1;
-                    float k0 = odd ? acc[2] : acc[0], k1 = odd ? acc[3] : acc[1];
-                    k0 += __shfl_xor_sync(0xffffffffu, odd ? acc[0] : acc[2], 1);
-                    k1 += __shfl_xor_sync(0xffffffffu, odd ? acc[1] : acc[3], 1);
-                    dx[(4 * gr + 2 * q) * PAD + cl].x = k0;
-                    dx[(4 * gr + 2 * q + 1) * PAD + cl].x = k1;
+                for (int i = 0; i < 2; ++i) {
+                    v[2 * i] = acc[0][i].x + __shfl_xor_sync(0xffffffffu, acc[1][i].x, LPC / 2);
+                    v[2 * i + 1] = acc[0][i].y + __shfl_xor_sync(0xffffffffu, acc[1][i].y, LPC / 2);
+                }
+                if constexpr (LPC == 2) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) ys[it & 3][2 * gr + i][TL::col8(cl[0], 2 * gr + i)] = make_float2(v[2 * i], v[2 * i + 1]);
                 } else {
+                    const int up = q & 1;
+                    float k0 = up ? v[2] : v[0], k1 = up ? v[3] : v[1];
+                    k0 += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 1);
+                    k1 += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 1);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) dx[(4 * gr + i) * PAD + cl].x = acc[i];
-                }
-            }
-        }
-        // the other buffer was last read before the barrier of the tile before
-        // (its y by this thread alone, at the places it now writes)
-        if (more) stage(t + TT, buf ^ 1);
-        __syncthreads();
-        if constexpr (FULL) {
-            if (stages && t + sr < p.t1) {
-                float o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float y = fmaf(Dv[j], u_now.get(j), dx[sr * PAD + 8 * sv + j].x);
-                    if (a.z) {
-                        const float zv = z_now.get(j);
-                        y *= zv * sigmoid_f(zv);
+                    for (int o = 2; o < LPC / 2; o <<= 1) {
+                        k0 += __shfl_xor_sync(0xffffffffu, k0, o);
+                        k1 += __shfl_xor_sync(0xffffffffu, k1, o);
                     }
-                    o[j] = y;
+                    ys[it & 3][2 * gr + up][TL::col8(cl[0], 2 * gr + up)] = make_float2(k0, k1);
                 }
-                Raw8<T>::store(yp + (int64_t)(t + sr) * a.E, o);
             }
-            u_now = u_next;
-            z_now = z_next;
+            if constexpr (MODE == kCkptG) {
+                // a backward piece ends behind these rows, or with the sequence
+                const int row = t + 4 * gr + 4 - p.s0;
+                if (row % a.bseg == 0 || row >= p.s1 - p.s0) {
+                    const int64_t i = (int64_t)p.r * pieces_per(a.L, a.bseg) + (row - 1) / a.bseg;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (live[j]) {
+                            const float g[4] = {Gl[j][0].x + Gl[j][0].y, Gl[j][1].x + Gl[j][1].y, Gl[j][2].x + Gl[j][2].y, Gl[j][3].x + Gl[j][3].y};
+                            put4(a.gl + i * st_all + st[j], g);
+                            if (q == 0) a.gsdt[i * a.E + e0 + cl[j]] = sdt[j];
+                        }
+                    restart();
+                }
+            }
+        };
+        if (groups == TT / 4 && !(PACKED && OUT && keep < t + TT)) {
+#pragma unroll
+            for (int gr = 0; gr < TT / 4; ++gr) walk4(gr, std::false_type{});
+        } else {
+#pragma unroll 1
+            for (int gr = 0; gr < groups; ++gr) walk4(gr, std::integral_constant<bool, PACKED && OUT>{});
         }
+        bar_arrive<kDone>(buf);
     }
 
-    if constexpr (FULL) {
-        if (p.t1 == p.s1) {
-            if constexpr (PACKED) {
-                const int slot = slot_at(sl, sl.slot_of[p.s1 - 1]);
-                if (slot >= 0 && live) store_h(a.final_state + slot * st_all + st);
-            } else if (live && a.final_state) {
-                store_h(a.final_state + p.r * st_all + st);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (OUT) {
+            if (p.t1 == p.s1) {
+                if constexpr (PACKED) {
+                    const int slot = slot_at(sl, sl.slot_of[p.s1 - 1]);
+                    if (slot >= 0 && live[j]) put4(a.final_state + slot * st_all + st[j], h[j]);
+                } else if (live[j] && a.final_state) {
+                    put4(a.final_state + p.r * st_all + st[j], h[j]);
+                }
             }
+        } else if (MODE == kLocal && live[j]) {
+            put4(ws.h + p.idx * st_all + st[j], h[j]);
+            if (q == 0) ws.sdt[p.idx * a.E + e0 + cl[j]] = sdt[j];
         }
-    } else if (MODE == kLocal && live) {
-        store_h(ws.h + p.idx * st_all + st);
-        if (q == 0) ws.sdt[p.idx * a.E + e] = sdt;
     }
 }
 
-constexpr int kWarpsWanted = 148 * 8;   // per device, below which rows are cut
+// Where rows are cut.  Nanoseconds a token for 1, 2, 3, 4 and 8 CTAs of 32
+// channels on each SM (bf16, gated): 79, 93, 111, 132, 258; the first walk takes
+// about two thirds of that.  One CTA to an SM gains from 4 pieces (79 L to
+// 222 L / 4), two do not (93 L to 222 L / 2).
+constexpr int kWarpsWanted = 148 * 8;   // walking warps of a cut scan
+constexpr int kPiecesLeast = 3;
 constexpr int kPieceLeast = 128;        // rows; a shorter piece costs more to join than it gains
 
 // Rows per piece, or no cut (the rows' count): one sequence that had all the
 // rows would get as many pieces as fill the device; sequences shorter than a
-// piece stay whole.
+// piece stay whole (packed ones are cut into pieces of up to twice that).
 int piece_rows(int nseq, int rows, int E, int N, int G)
 {
-    const int ch = kThreads / diag_lanes(N);
-    const int64_t ctas = (int64_t)((E / G + ch - 1) / ch) * G;
-    const int64_t pieces = kWarpsWanted / (ctas * (kThreads / 32));
-    if (pieces < 2) return rows;
+    const int ch = kWarps * 64 / tile_lanes(N);
+    const int64_t pieces = kWarpsWanted / ((int64_t)channel_tiles(E, G, ch) * G * kWarps);
+    if (pieces < kPiecesLeast) return rows;
     int64_t seg = (rows + pieces - 1) / pieces;
     seg = (seg + 31) / 32 * 32;
     if (seg < kPieceLeast) seg = kPieceLeast;
@@ -345,11 +543,15 @@ int64_t piece_count(bool packed, int nseq, int L, int rows, int seg)
 template <typename T, int LPC, bool PACKED, Mode MODE, bool CUT>
 cudaError_t launch_mode(const DiagArgs& a, int seg, int64_t pieces, cudaStream_t s)
 {
-    constexpr int smem = (int)sizeof(Smem<LPC>);
-    static_assert(smem <= 48 * 1024, "no opt-in needed");
-    const int per_group = a.E / a.G, CH = Tile<LPC>::CH;
-    const dim3 grid((unsigned)pieces, (unsigned)((per_group + CH - 1) / CH * a.G));
-    diag_scan_kernel<T, LPC, PACKED, MODE, CUT><<<grid, kThreads, smem, s>>>(a, seg, pieces);
+    const int64_t grid = pieces * channel_tiles(a.E, a.G, DiagTile<LPC, kWarps>::CH) * a.G;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    constexpr int smem = (int)sizeof(Smem<T, LPC, MODE>);
+    if (smem > 32 * 1024) {   // with the kernel's own arrays, beyond what needs no leave
+        const cudaError_t e = cudaFuncSetAttribute((const void*)diag_scan_kernel<T, LPC, PACKED, MODE, CUT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    diag_scan_kernel<T, LPC, PACKED, MODE, CUT><<<(unsigned)grid, kThreads, smem, s>>>(a, seg, pieces);
     return cudaGetLastError();
 }
 
@@ -364,10 +566,13 @@ cudaError_t launch_lpc(const DiagArgs& a, int seg, cudaStream_t s)
 }
 
 template <typename T, bool PACKED, Mode MODE>
-cudaError_t launch_t(const DiagArgs& a, int seg, cudaStream_t s)
+cudaError_t launch_t(const DiagArgs& args, int seg, cudaStream_t s)
 {
-    switch (diag_lanes(a.N)) {
-        case 1: return launch_lpc<T, 1, PACKED, MODE>(a, seg, s);
+    DiagArgs a = args;
+    constexpr uintptr_t four = 4 * sizeof(T);
+    a.longest_first = PACKED && a.nseq > 1 && a.nseq <= kSortSeqs && a.rows / a.nseq >= kSortRows;
+    a.bc_aligned = a.bcs % 4 == 0 && reinterpret_cast<uintptr_t>(a.B) % four == 0 && reinterpret_cast<uintptr_t>(a.C) % four == 0;
+    switch (tile_lanes(a.N)) {
         case 2: return launch_lpc<T, 2, PACKED, MODE>(a, seg, s);
         case 4: return launch_lpc<T, 4, PACKED, MODE>(a, seg, s);
         case 8: return launch_lpc<T, 8, PACKED, MODE>(a, seg, s);
@@ -392,9 +597,20 @@ cudaError_t launch_diag_scan(const DiagArgs& a, cudaStream_t s)
     return a.bf16 ? launch_t<__nv_bfloat16, false, kOutput>(a, seg, s) : launch_t<float, false, kOutput>(a, seg, s);
 }
 
-cudaError_t launch_diag_ckpt(const DiagArgs& a, int seg, cudaStream_t s)
+cudaError_t launch_diag_ckpt(const DiagArgs& a, cudaStream_t s)
 {
+    const int seg = diag_ckpt_rows(a.nseq, a.L, a.E, a.N, a.G, a.bseg);
+    if (a.bseg < a.L) return a.bf16 ? launch_t<__nv_bfloat16, false, kCkptG>(a, seg, s) : launch_t<float, false, kCkptG>(a, seg, s);
     return a.bf16 ? launch_t<__nv_bfloat16, false, kCkpt>(a, seg, s) : launch_t<float, false, kCkpt>(a, seg, s);
+}
+
+// Rows per piece of the walk that keeps states: as the forward scan's, in
+// whole backward pieces.
+int diag_ckpt_rows(int b, int L, int E, int N, int G, int bseg)
+{
+    const int64_t seg = piece_rows(b, b * L, E, N, G);
+    const int64_t whole = (seg + bseg - 1) / bseg * bseg;
+    return seg < L && whole < L ? (int)whole : L;
 }
 
 size_t diag_cut_bytes(int nseq, int64_t pieces, int E, int N) { return cut_ws_bytes(nseq, pieces, E, N); }

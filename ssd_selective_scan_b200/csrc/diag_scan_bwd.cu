@@ -32,8 +32,7 @@
 //
 // Bound by instruction issue, not by HBM: per token, channel and state 2
 // exponentials (one per walk) and about 20 other instructions.
-#include "diag.cuh"
-#include "diag.h"
+#include "diag_tile.cuh"
 
 namespace ssd {
 namespace {
@@ -42,26 +41,8 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// lanes per channel: at least 2 here (a tile of one-lane channels would be
-// wider than the CTA's loads; N <= 4 leaves the second lane's states empty)
-inline int bwd_lanes(int N) { return diag_lanes(N) < 2 ? 2 : diag_lanes(N); }
-
-template <int LPC> struct Tile {
-    static constexpr int NL = 32 / LPC;                   // channel lanes of a warp
-    static constexpr int CH = kWarps * 2 * NL;            // channels per CTA
-    static constexpr int TT = LPC == 2 ? 8 : 16;          // rows per tile
-    static constexpr int NP = 4 * LPC;                    // states, padded
-    static constexpr int VPR = CH / 8;                    // 8-element vectors per row
-    static constexpr int NVEC = TT * VPR;
-    static_assert(NVEC <= kThreads && TT % kDiagCkpt == 0, "");
-    // where channel c of a row lies: the 8 channels that one thread writes
-    // are rotated by their vector's number, so that the 8 vectors' writes
-    // fall into different banks; 8 channels read together stay together
-    __device__ static int col(int c) { return (c & ~7) | ((c ^ (c >> 3)) & 7); }
-};
-
 template <typename T, int LPC> struct Smem {
-    using TL = Tile<LPC>;
+    using TL = DiagTile<LPC, kWarps>;
     float4 tile[TL::TT][TL::CH];              // dt, x -> gB, p, w A
     float ysum[TL::TT][TL::CH];
     float4 B[TL::TT][LPC], C[TL::TT][LPC];
@@ -69,40 +50,27 @@ template <typename T, int LPC> struct Smem {
     T raw[2][4][TL::TT][TL::CH];              // u, dt_raw, dy, z
 };
 
-__device__ inline void cp16(void* smem, const void* gmem)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");
-}
-__device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Partial sums and kept states in the workspace.
+// Kept states and partial sums in the workspace.
 struct BwdWs {
-    float *ckpt, *cut, *g, *dA, *dD, *dbias, *bc;
+    float *ckpt, *cut, *gl, *gsdt, *dA, *dD, *dbias, *bc;
 };
 
-// GRAD: the gradients.  Otherwise only the piece's own part of G at its start
-// (from dfinal in a sequence's last piece, from zero in the others).
-template <typename T, int LPC, bool GRAD>
-__global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba, const BwdWs ws, int seg, int64_t pieces)
+template <typename T, int LPC>
+__global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba, const BwdWs ws, int seg)
 {
-    using TL = Tile<LPC>;
-    constexpr int NL = TL::NL, CH = TL::CH, TT = TL::TT, VPR = TL::VPR, NP = TL::NP;
+    using TL = DiagTile<LPC, kWarps>;
+    constexpr int NL = TL::NL, TT = TL::TT, VPR = TL::VPR, NP = TL::NP, NBC = TL::NBC;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Smem<T, LPC>& sm = *reinterpret_cast<Smem<T, LPC>*>(smem_raw);
     const DiagArgs& a = ba.f;
 
     Piece p;
     find_piece_dense(blockIdx.x, a.L, seg, p);
-    const bool head = p.t0 == p.s0, tail = p.t1 == p.s1;
-    if (!GRAD && head) return;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = lane % LPC, cg = lane / LPC;
-    const int per_group = a.E / a.G, tiles = (per_group + CH - 1) / CH;
-    const int grp = blockIdx.y / tiles;
-    const int e0 = grp * per_group + (blockIdx.y - grp * tiles) * CH;
-    const int e_end = min(e0 + CH, (grp + 1) * per_group);
+    const ChannelTile ct(a.E, a.G, TL::CH, blockIdx.y);
+    const int e0 = ct.e0, e_end = ct.e_end;
     const int n0 = 4 * q;
     const int64_t st_all = (int64_t)a.E * a.N;
     int cl[2], col[2];
@@ -111,8 +79,8 @@ __global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba
     float2 A2[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        cl[j] = warp * 2 * NL + j * NL + cg;
-        col[j] = TL::col(cl[j]);
+        cl[j] = TL::channel(warp, lane, j);
+        col[j] = TL::col16(cl[j], 0);
         live[j] = e0 + cl[j] < e_end && n0 < a.N;
         st[j] = (int64_t)(e0 + cl[j]) * a.N + n0;
         A2[j][0] = A2[j][1] = make_float2(0.0f, 0.0f);
@@ -123,29 +91,26 @@ __global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba
         }
     }
 
-    // G behind the piece's last row
+    // G behind the piece's last row: dfinal, folded over the pieces behind
     float2 G[2][2], dA[2][2];
-    const float* cut_sdt = ws.cut ? ws.cut + pieces * st_all : nullptr;
     const int64_t last = p.first + pieces_per(a.L, seg) - 1;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         G[j][0] = G[j][1] = dA[j][0] = dA[j][1] = make_float2(0.0f, 0.0f);
         if (!live[j]) continue;
-        const float* src = tail ? (ba.dfinal ? ba.dfinal + p.r * st_all : nullptr) : GRAD ? ws.g + last * st_all : nullptr;
-        if (src) {
-            const float4 v = *reinterpret_cast<const float4*>(src + st[j]);
+        if (ba.dfinal) {
+            const float4 v = *reinterpret_cast<const float4*>(ba.dfinal + p.r * st_all + st[j]);
             G[j][0] = make_float2(v.x, v.y);
             G[j][1] = make_float2(v.z, v.w);
         }
-        if (GRAD && !tail)
-            for (int64_t i = last - 1; i > p.idx; --i) {
-                const float sdt = cut_sdt[i * a.E + e0 + cl[j]];
-                const float4 v = *reinterpret_cast<const float4*>(ws.g + i * st_all + st[j]);
-                G[j][0].x = fmaf(ex2(A2[j][0].x * sdt), G[j][0].x, v.x);
-                G[j][0].y = fmaf(ex2(A2[j][0].y * sdt), G[j][0].y, v.y);
-                G[j][1].x = fmaf(ex2(A2[j][1].x * sdt), G[j][1].x, v.z);
-                G[j][1].y = fmaf(ex2(A2[j][1].y * sdt), G[j][1].y, v.w);
-            }
+        for (int64_t i = last; i > p.idx; --i) {
+            const float sdt = ws.gsdt[i * a.E + e0 + cl[j]];
+            const float4 v = *reinterpret_cast<const float4*>(ws.gl + i * st_all + st[j]);
+            G[j][0].x = fmaf(ex2(A2[j][0].x * sdt), G[j][0].x, v.x);
+            G[j][0].y = fmaf(ex2(A2[j][0].y * sdt), G[j][0].y, v.y);
+            G[j][1].x = fmaf(ex2(A2[j][1].x * sdt), G[j][1].x, v.z);
+            G[j][1].y = fmaf(ex2(A2[j][1].y * sdt), G[j][1].y, v.w);
+        }
     }
 
     // loading: vector sv of row sr of each tile
@@ -159,43 +124,31 @@ __global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba
         bias[j] = loads && a.dt_bias ? a.dt_bias[ev + j] : 0.0f;
         dDs[j] = dbs[j] = 0.0f;
     }
-    const T* Bp = static_cast<const T*>(a.B) + (int64_t)grp * a.N;
-    const T* Cp = static_cast<const T*>(a.C) + (int64_t)grp * a.N;
+    const T* Bp = static_cast<const T*>(a.B) + (int64_t)ct.group * a.N;
+    const T* Cp = static_cast<const T*>(a.C) + (int64_t)ct.group * a.N;
     const bool gated = a.z != nullptr;
 
     auto fetch = [&](int t, int buf) {
-        const int row = t + sr;
+        const int64_t row = t + sr;
         if (loads && row < p.t1) {
-            const T* src[4] = {static_cast<const T*>(a.u) + (int64_t)row * a.us + ev, static_cast<const T*>(a.dt) + (int64_t)row * a.dts + ev,
-                               static_cast<const T*>(ba.dy) + (int64_t)row * a.E + ev,
-                               static_cast<const T*>(a.z) + (int64_t)row * a.zs + ev};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i == 3 && !gated) break;
-#pragma unroll
-                for (int k = 0; k < (int)sizeof(T) / 2; ++k) cp16(&sm.raw[buf][i][sr][8 * sv + k * (16 / sizeof(T))], src[i] + k * (16 / sizeof(T)));
-            }
+            cp_row8(&sm.raw[buf][0][sr][8 * sv], static_cast<const T*>(a.u) + row * a.us + ev);
+            cp_row8(&sm.raw[buf][1][sr][8 * sv], static_cast<const T*>(a.dt) + row * a.dts + ev);
+            cp_row8(&sm.raw[buf][2][sr][8 * sv], static_cast<const T*>(ba.dy) + row * a.E + ev);
+            if (gated) cp_row8(&sm.raw[buf][3][sr][8 * sv], static_cast<const T*>(a.z) + row * a.zs + ev);
         }
         cp_commit();
     };
-    constexpr int NBC = (TT * NP + kThreads - 1) / kThreads;
     float bq[NBC], cq[NBC];
     auto fetch_bc = [&](int t) {
 #pragma unroll
         for (int i = 0; i < NBC; ++i) {
             const int k = tid + i * kThreads, row = k / NP, n = k % NP;
             const bool ok = k < TT * NP && t + row < p.t1 && n < a.N;
-            bq[i] = GRAD && ok ? ld_f(Bp + (int64_t)(t + row) * a.bcs + n) : 0.0f;
+            bq[i] = ok ? ld_f(Bp + (int64_t)(t + row) * a.bcs + n) : 0.0f;
             cq[i] = ok ? ld_f(Cp + (int64_t)(t + row) * a.bcs + n) : 0.0f;
         }
     };
-    auto raw8 = [&](int buf, int i) {
-        Raw8<T> r;
-        const uint4* src = reinterpret_cast<const uint4*>(&sm.raw[buf][i][sr][8 * sv]);
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.q[k] = src[k];
-        return r;
-    };
+    auto raw8 = [&](int buf, int i) { return smem_row8(&sm.raw[buf][i][sr][8 * sv]); };
 
     const int ntile = (p.t1 - p.t0 + TT - 1) / TT;
     const int64_t ck0 = (int64_t)p.r * ckpts_of(a.L) + (p.t0 - p.s0) / kDiagCkpt;   // the piece's first kept state
@@ -204,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba
     int buf = 0;
     for (int it = ntile - 1; it >= 0; --it, buf ^= 1) {
         const int t = p.t0 + it * TT;
-        cp_wait<0>();   // a thread reads back what it copied itself
+        cp_wait_all();   // a thread reads back what it copied itself
         if (tid < TL::NVEC) {
             const bool ok = loads && t + sr < p.t1;
             const Raw8<T> u = raw8(buf, 0), v = raw8(buf, 1), dy = raw8(buf, 2), z = raw8(buf, 3);
@@ -217,14 +170,14 @@ __global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba
                     f.z = dy.get(j);
                     if (gated) f.z *= z.get(j) * sigmoid_f(z.get(j));
                 }
-                sm.tile[sr][TL::col(8 * sv + j)] = f;
+                sm.tile[sr][TL::col16(8 * sv + j, 0)] = f;
             }
         }
 #pragma unroll
         for (int i = 0; i < NBC; ++i) {
             const int k = tid + i * kThreads;
             if (k < TT * NP) {
-                if (GRAD) reinterpret_cast<float*>(sm.B)[k] = bq[i];
+                reinterpret_cast<float*>(sm.B)[k] = bq[i];
                 reinterpret_cast<float*>(sm.C)[k] = cq[i];
             }
         }
@@ -234,141 +187,124 @@ __global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba
             fetch_bc(t - TT);
         }
 
-        if constexpr (!GRAD) {
-#pragma unroll 4
-            for (int i = TT - 1; i >= 0; --i) {
-                const float4 c4 = sm.C[i][q];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float4 d = sm.tile[i][col[j]];
-                    const float2 pp = make_float2(d.z, d.z), dd = make_float2(d.x, d.x);
-                    const float2 s0 = pk_mul(A2[j][0], dd), s1 = pk_mul(A2[j][1], dd);
-                    const float2 g0 = pk_fma(make_float2(c4.x, c4.y), pp, G[j][0]), g1 = pk_fma(make_float2(c4.z, c4.w), pp, G[j][1]);
-                    G[j][0] = pk_mul(make_float2(ex2(s0.x), ex2(s0.y)), g0);
-                    G[j][1] = pk_mul(make_float2(ex2(s1.x), ex2(s1.y)), g1);
-                }
-            }
-            __syncthreads();
-        } else {
 #pragma unroll 1
-            for (int half = TT / kDiagCkpt - 1; half >= 0; --half) {
-                const int r0 = half * kDiagCkpt;
-                if (t + r0 >= p.t1) continue;
-                // forward over 8 rows: decays and states
-                float2 av[kDiagCkpt][2][2], hv[kDiagCkpt + 1][2][2];
-                const float* ck = ws.ckpt + (ck0 + (it * TT + r0) / kDiagCkpt) * st_all;
+        for (int half = TT / kDiagCkpt - 1; half >= 0; --half) {
+            const int r0 = half * kDiagCkpt;
+            if (t + r0 >= p.t1) continue;
+            // forward over 8 rows: decays and states
+            float2 av[kDiagCkpt][2][2], hv[kDiagCkpt + 1][2][2];
+            const float* ck = ws.ckpt + (ck0 + (it * TT + r0) / kDiagCkpt) * st_all;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (live[j]) v = __ldcs(reinterpret_cast<const float4*>(ck + st[j]));
+                hv[0][j][0] = make_float2(v.x, v.y);
+                hv[0][j][1] = make_float2(v.z, v.w);
+            }
+#pragma unroll
+            for (int i = 0; i < kDiagCkpt; ++i) {
+                const float4 b4 = sm.B[r0 + i][q];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (live[j]) v = __ldcs(reinterpret_cast<const float4*>(ck + st[j]));
-                    hv[0][j][0] = make_float2(v.x, v.y);
-                    hv[0][j][1] = make_float2(v.z, v.w);
-                }
-#pragma unroll
-                for (int i = 0; i < kDiagCkpt; ++i) {
-                    const float4 b4 = sm.B[r0 + i][q];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float2 d = *reinterpret_cast<const float2*>(&sm.tile[r0 + i][col[j]]);
-                        const float2 dd = make_float2(d.x, d.x), xx = make_float2(d.y, d.y);
-                        const float2 s0 = pk_mul(A2[j][0], dd), s1 = pk_mul(A2[j][1], dd);
-                        av[i][j][0] = make_float2(ex2(s0.x), ex2(s0.y));
-                        av[i][j][1] = make_float2(ex2(s1.x), ex2(s1.y));
-                        hv[i + 1][j][0] = pk_fma(av[i][j][0], hv[i][j][0], pk_mul(make_float2(b4.x, b4.y), xx));
-                        hv[i + 1][j][1] = pk_fma(av[i][j][1], hv[i][j][1], pk_mul(make_float2(b4.z, b4.w), xx));
-                    }
-                }
-                // and back
-#pragma unroll
-                for (int i = kDiagCkpt - 1; i >= 0; --i) {
-                    const int row = r0 + i;
-                    const float4 b4 = sm.B[row][q], c4 = sm.C[row][q];
-                    const float2 b01 = make_float2(b4.x, b4.y), b23 = make_float2(b4.z, b4.w);
-                    const float2 c01 = make_float2(c4.x, c4.y), c23 = make_float2(c4.z, c4.w);
-                    float sn[4], sy[2];       // state sums: gB, w A of each channel; y
-                    float2 sB[2], sC[2];      // channel sums
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float4 d = sm.tile[row][col[j]];
-                        const float2 pp = make_float2(d.z, d.z), xx = make_float2(d.y, d.y), dd = make_float2(d.x, d.x);
-                        const float2 g0 = pk_fma(c01, pp, G[j][0]), g1 = pk_fma(c23, pp, G[j][1]);
-                        const float2 gb = pk_fma(g0, b01, pk_mul(g1, b23));
-                        sn[2 * j] = gb.x + gb.y;
-                        if (j == 0) {
-                            sB[0] = pk_mul(g0, xx); sB[1] = pk_mul(g1, xx);
-                            sC[0] = pk_mul(hv[i + 1][j][0], pp); sC[1] = pk_mul(hv[i + 1][j][1], pp);
-                        } else {
-                            sB[0] = pk_fma(g0, xx, sB[0]); sB[1] = pk_fma(g1, xx, sB[1]);
-                            sC[0] = pk_fma(hv[i + 1][j][0], pp, sC[0]); sC[1] = pk_fma(hv[i + 1][j][1], pp, sC[1]);
-                        }
-                        G[j][0] = pk_mul(av[i][j][0], g0);
-                        G[j][1] = pk_mul(av[i][j][1], g1);
-                        const float2 w0 = pk_mul(G[j][0], hv[i][j][0]), w1 = pk_mul(G[j][1], hv[i][j][1]);
-                        dA[j][0] = pk_fma(w0, dd, dA[j][0]);
-                        dA[j][1] = pk_fma(w1, dd, dA[j][1]);
-                        const float2 wa = pk_fma(w0, A2[j][0], pk_mul(w1, A2[j][1]));
-                        sn[2 * j + 1] = wa.x + wa.y;
-                        if (gated) {
-                            const float2 yy = pk_fma(hv[i + 1][j][0], c01, pk_mul(hv[i + 1][j][1], c23));
-                            sy[j] = yy.x + yy.y;
-                        }
-                    }
-                    float sc[8] = {sB[0].x, sB[0].y, sB[1].x, sB[1].y, sC[0].x, sC[0].y, sC[1].x, sC[1].y};
-                    int at = 0;
-                    scatter_sum<8, NL, LPC>(sc, cg, at);
-#pragma unroll
-                    for (int k = 0; k < (NL < 8 ? 8 / NL : 1); ++k)
-                        reinterpret_cast<float*>(&sm.red[warp][row][n0 + ((at + k) & 3)])[(at + k) >> 2] = sc[k];
-                    at = 0;
-                    scatter_sum<4, LPC, 1>(sn, q, at);
-#pragma unroll
-                    for (int k = 0; k < (LPC < 4 ? 4 / LPC : 1); ++k) {
-                        const int i2 = at + k;
-                        reinterpret_cast<float*>(&sm.tile[row][col[i2 >> 1]])[i2 & 1 ? 3 : 1] = sn[k];
-                    }
-                    if (gated) {
-                        at = 0;
-                        scatter_sum<2, LPC, 1>(sy, q, at);
-                        sm.ysum[row][col[at]] = sy[0];
-                    }
+                    const float2 d = *reinterpret_cast<const float2*>(&sm.tile[r0 + i][col[j]]);
+                    const float2 dd = make_float2(d.x, d.x), xx = make_float2(d.y, d.y);
+                    const float2 s0 = pk_mul(A2[j][0], dd), s1 = pk_mul(A2[j][1], dd);
+                    av[i][j][0] = make_float2(ex2(s0.x), ex2(s0.y));
+                    av[i][j][1] = make_float2(ex2(s1.x), ex2(s1.y));
+                    hv[i + 1][j][0] = pk_fma(av[i][j][0], hv[i][j][0], pk_mul(make_float2(b4.x, b4.y), xx));
+                    hv[i + 1][j][1] = pk_fma(av[i][j][1], hv[i][j][1], pk_mul(make_float2(b4.z, b4.w), xx));
                 }
             }
-            __syncthreads();
-            // the loading threads finish their 8 channels of a row
-            if (loads && t + sr < p.t1) {
-                const Raw8<T> u = raw8(buf, 0), v = raw8(buf, 1), dy = raw8(buf, 2), z = raw8(buf, 3);
-                float du[8], ddt[8], dz[8];
+            // and back
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = TL::col(8 * sv + j);
-                    const float4 f = sm.tile[sr][c];
-                    const float uv = u.get(j);
-                    du[j] = fmaf(Dv[j], f.z, f.x * f.y);
-                    ddt[j] = fmaf(uv, f.y, f.w * kLn2) * sigmoid_f(v.get(j) + bias[j]);
-                    dDs[j] = fmaf(uv, f.z, dDs[j]);
-                    dbs[j] += ddt[j];
+            for (int i = kDiagCkpt - 1; i >= 0; --i) {
+                const int row = r0 + i;
+                const float4 b4 = sm.B[row][q], c4 = sm.C[row][q];
+                const float2 b01 = make_float2(b4.x, b4.y), b23 = make_float2(b4.z, b4.w);
+                const float2 c01 = make_float2(c4.x, c4.y), c23 = make_float2(c4.z, c4.w);
+                float sn[4], sy[2];       // state sums: gB, w A of each channel; y
+                float2 sB[2], sC[2];      // channel sums
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float4 d = sm.tile[row][col[j]];
+                    const float2 pp = make_float2(d.z, d.z), xx = make_float2(d.y, d.y), dd = make_float2(d.x, d.x);
+                    const float2 g0 = pk_fma(c01, pp, G[j][0]), g1 = pk_fma(c23, pp, G[j][1]);
+                    const float2 gb = pk_fma(g0, b01, pk_mul(g1, b23));
+                    sn[2 * j] = gb.x + gb.y;
+                    if (j == 0) {
+                        sB[0] = pk_mul(g0, xx); sB[1] = pk_mul(g1, xx);
+                        sC[0] = pk_mul(hv[i + 1][j][0], pp); sC[1] = pk_mul(hv[i + 1][j][1], pp);
+                    } else {
+                        sB[0] = pk_fma(g0, xx, sB[0]); sB[1] = pk_fma(g1, xx, sB[1]);
+                        sC[0] = pk_fma(hv[i + 1][j][0], pp, sC[0]); sC[1] = pk_fma(hv[i + 1][j][1], pp, sC[1]);
+                    }
+                    G[j][0] = pk_mul(av[i][j][0], g0);
+                    G[j][1] = pk_mul(av[i][j][1], g1);
+                    const float2 w0 = pk_mul(G[j][0], hv[i][j][0]), w1 = pk_mul(G[j][1], hv[i][j][1]);
+                    dA[j][0] = pk_fma(w0, dd, dA[j][0]);
+                    dA[j][1] = pk_fma(w1, dd, dA[j][1]);
+                    const float2 wa = pk_fma(w0, A2[j][0], pk_mul(w1, A2[j][1]));
+                    sn[2 * j + 1] = wa.x + wa.y;
                     if (gated) {
-                        const float zv = z.get(j);
-                        dz[j] = dy.get(j) * fmaf(Dv[j], uv, sm.ysum[sr][c]) * dsilu_f(zv, sigmoid_f(zv));
+                        const float2 yy = pk_fma(hv[i + 1][j][0], c01, pk_mul(hv[i + 1][j][1], c23));
+                        sy[j] = yy.x + yy.y;
                     }
                 }
-                const int64_t o = (int64_t)(t + sr) * a.E + ev;
-                Raw8<T>::store(static_cast<T*>(ba.du) + o, du);
-                Raw8<T>::store(static_cast<T*>(ba.ddt) + o, ddt);
-                if (gated) Raw8<T>::store(static_cast<T*>(ba.dz) + o, dz);
-            }
-            const int rows = min(TT, p.t1 - t);
-            for (int k = tid; k < rows * NP; k += kThreads) {
-                const int row = k / NP, n = k % NP;
-                if (n < a.N) {
-                    float2 s = sm.red[0][row][n];
+                float sc[8] = {sB[0].x, sB[0].y, sB[1].x, sB[1].y, sC[0].x, sC[0].y, sC[1].x, sC[1].y};
+                int at = 0;
+                scatter_sum<8, NL, LPC>(sc, cg, at);
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w) {
-                        s.x += sm.red[w][row][n].x;
-                        s.y += sm.red[w][row][n].y;
-                    }
-                    reinterpret_cast<float2*>(ws.bc)[((int64_t)blockIdx.y * a.rows + t + row) * a.N + n] = s;
+                for (int k = 0; k < (NL < 8 ? 8 / NL : 1); ++k)
+                    reinterpret_cast<float*>(&sm.red[warp][row][n0 + ((at + k) & 3)])[(at + k) >> 2] = sc[k];
+                // every lane keeps the channel of its slot 0 (diag_tile.cuh)
+                float v[2] = {sn[0] + __shfl_xor_sync(0xffffffffu, sn[2], LPC / 2), sn[1] + __shfl_xor_sync(0xffffffffu, sn[3], LPC / 2)};
+                at = 0;
+                scatter_sum<2, LPC / 2, 1>(v, q % (LPC / 2), at);
+#pragma unroll
+                for (int k = 0; k < (LPC == 2 ? 2 : 1); ++k) reinterpret_cast<float*>(&sm.tile[row][col[0]])[2 * (at + k) + 1] = v[k];
+                if (gated) {
+                    float y = sy[0] + __shfl_xor_sync(0xffffffffu, sy[1], LPC / 2);
+#pragma unroll
+                    for (int o = LPC / 4; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                    sm.ysum[row][col[0]] = y;
                 }
+            }
+        }
+        __syncthreads();
+        // the loading threads finish their 8 channels of a row
+        if (loads && t + sr < p.t1) {
+            const Raw8<T> u = raw8(buf, 0), v = raw8(buf, 1), dy = raw8(buf, 2), z = raw8(buf, 3);
+            float du[8], ddt[8], dz[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = TL::col16(8 * sv + j, 0);
+                const float4 f = sm.tile[sr][c];
+                const float uv = u.get(j);
+                du[j] = fmaf(Dv[j], f.z, f.x * f.y);
+                ddt[j] = fmaf(uv, f.y, f.w * kLn2) * sigmoid_f(v.get(j) + bias[j]);
+                dDs[j] = fmaf(uv, f.z, dDs[j]);
+                dbs[j] += ddt[j];
+                if (gated) {
+                    const float zv = z.get(j);
+                    dz[j] = dy.get(j) * fmaf(Dv[j], uv, sm.ysum[sr][c]) * dsilu_f(zv, sigmoid_f(zv));
+                }
+            }
+            const int64_t o = (int64_t)(t + sr) * a.E + ev;
+            Raw8<T>::store(static_cast<T*>(ba.du) + o, du);
+            Raw8<T>::store(static_cast<T*>(ba.ddt) + o, ddt);
+            if (gated) Raw8<T>::store(static_cast<T*>(ba.dz) + o, dz);
+        }
+        const int rows = min(TT, p.t1 - t);
+        for (int k = tid; k < rows * NP; k += kThreads) {
+            const int row = k / NP, n = k % NP;
+            if (n < a.N) {
+                float2 s = sm.red[0][row][n];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    s.x += sm.red[w][row][n].x;
+                    s.y += sm.red[w][row][n].y;
+                }
+                reinterpret_cast<float2*>(ws.bc)[((int64_t)blockIdx.y * a.rows + t + row) * a.N + n] = s;
             }
         }
     }
@@ -376,32 +312,26 @@ __global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (!live[j]) continue;
-        const float4 v = make_float4(G[j][0].x, G[j][0].y, G[j][1].x, G[j][1].y);
-        if constexpr (!GRAD) {
-            *reinterpret_cast<float4*>(ws.g + p.idx * st_all + st[j]) = v;
-        } else {
-            if (head && ba.dinit) *reinterpret_cast<float4*>(ba.dinit + p.r * st_all + st[j]) = v;
-            *reinterpret_cast<float4*>(ws.dA + p.idx * st_all + st[j]) = make_float4(dA[j][0].x, dA[j][0].y, dA[j][1].x, dA[j][1].y);
-        }
+        if (p.t0 == p.s0 && ba.dinit)
+            *reinterpret_cast<float4*>(ba.dinit + p.r * st_all + st[j]) = make_float4(G[j][0].x, G[j][0].y, G[j][1].x, G[j][1].y);
+        *reinterpret_cast<float4*>(ws.dA + p.idx * st_all + st[j]) = make_float4(dA[j][0].x, dA[j][0].y, dA[j][1].x, dA[j][1].y);
     }
-    if constexpr (GRAD) {
-        // dD, ddt_bias: over the tile's rows through shared memory
-        __syncthreads();
-        if (loads)
+    // dD, ddt_bias: over the tile's rows through shared memory
+    __syncthreads();
+    if (loads)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) *reinterpret_cast<float2*>(&sm.tile[sr][8 * sv + j]) = make_float2(dDs[j], dbs[j]);
-        __syncthreads();
-        for (int c = tid; c < e_end - e0; c += kThreads) {
-            float2 s = make_float2(0.0f, 0.0f);
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<float2*>(&sm.tile[sr][8 * sv + j]) = make_float2(dDs[j], dbs[j]);
+    __syncthreads();
+    for (int c = tid; c < e_end - e0; c += kThreads) {
+        float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int r = 0; r < TT; ++r) {
-                const float2 v = *reinterpret_cast<const float2*>(&sm.tile[r][c]);
-                s.x += v.x;
-                s.y += v.y;
-            }
-            ws.dD[p.idx * a.E + e0 + c] = s.x;
-            ws.dbias[p.idx * a.E + e0 + c] = s.y;
+        for (int r = 0; r < TT; ++r) {
+            const float2 v = *reinterpret_cast<const float2*>(&sm.tile[r][c]);
+            s.x += v.x;
+            s.y += v.y;
         }
+        ws.dD[p.idx * a.E + e0 + c] = s.x;
+        ws.dbias[p.idx * a.E + e0 + c] = s.y;
     }
 }
 
@@ -446,15 +376,17 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
     }
 }
 
-// Rows per piece: as the forward scan's, for this kernel's CTAs.
-constexpr int kCtasWanted = 148 * 2;
-constexpr int kPieceLeast = 128;
+// Rows per piece.  The kernel's time is that of its fullest SM, so the rows
+// are cut until the CTAs make kWaves of what the device holds at a time: a
+// last, partly filled wave then costs little.
+constexpr int kCtasAtATime = 148 * 2;
+constexpr int kWaves = 6;
+constexpr int kPieceLeast = 64;
 
 int bwd_piece_rows(int b, int L, int E, int N, int G)
 {
-    const int ch = 256 / bwd_lanes(N);
-    const int64_t ctas = (int64_t)b * ((E / G + ch - 1) / ch) * G;
-    const int64_t pieces = kCtasWanted / ctas;
+    const int64_t ctas = (int64_t)b * channel_tiles(E, G, kWarps * 64 / tile_lanes(N)) * G;
+    const int64_t pieces = (kCtasAtATime * kWaves + ctas - 1) / ctas;
     if (pieces < 2) return L;
     int64_t seg = ((int64_t)L + pieces - 1) / pieces;
     seg = (seg + 31) / 32 * 32;
@@ -465,7 +397,7 @@ int bwd_piece_rows(int b, int L, int E, int N, int G)
 struct Plan {
     int seg, tiles;
     int64_t pieces;
-    size_t ckpt, cut, g, dA, dD, dbias, bc, total;   // byte offsets
+    size_t ckpt, cut, gl, gsdt, dA, dD, dbias, bc, total;   // byte offsets
 };
 
 Plan plan_of(int b, int L, int E, int N, int G)
@@ -473,18 +405,18 @@ Plan plan_of(int b, int L, int E, int N, int G)
     Plan p{};
     p.seg = bwd_piece_rows(b, L, E, N, G);
     p.pieces = (int64_t)b * pieces_per(L, p.seg);
-    const int ch = 256 / bwd_lanes(N);
-    p.tiles = (E / G + ch - 1) / ch;
-    const bool cut = p.seg < L;
+    p.tiles = channel_tiles(E, G, kWarps * 64 / tile_lanes(N));
+    const int walk = diag_ckpt_rows(b, L, E, N, G, p.seg);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    const size_t state = (size_t)E * N * 4;
+    const size_t state = (size_t)E * N * 4, parts = (size_t)p.pieces;
     p.ckpt = 0;
     p.cut = p.ckpt + up((size_t)b * ckpts_of(L) * state);
-    p.g = p.cut + (cut ? up(diag_cut_bytes(b, p.pieces, E, N)) : 0);
-    p.dA = p.g + (cut ? up((size_t)p.pieces * state) : 0);
-    p.dD = p.dA + up((size_t)p.pieces * state);
-    p.dbias = p.dD + up((size_t)p.pieces * E * 4);
-    p.bc = p.dbias + up((size_t)p.pieces * E * 4);
+    p.gl = p.cut + (walk < L ? up(diag_cut_bytes(b, (int64_t)b * pieces_per(L, walk), E, N)) : 0);
+    p.gsdt = p.gl + (p.seg < L ? up(parts * state) : 0);
+    p.dA = p.gsdt + (p.seg < L ? up(parts * E * 4) : 0);
+    p.dD = p.dA + up(parts * state);
+    p.dbias = p.dD + up(parts * E * 4);
+    p.bc = p.dbias + up(parts * E * 4);
     p.total = p.bc + up((size_t)p.tiles * G * b * L * N * 8);
     return p;
 }
@@ -493,18 +425,11 @@ template <typename T, int LPC>
 cudaError_t launch_lpc(const DiagBwdArgs& a, const Plan& p, const BwdWs& ws, cudaStream_t s)
 {
     const int smem = (int)sizeof(Smem<T, LPC>);
-    const dim3 grid((unsigned)p.pieces, (unsigned)(p.tiles * a.f.G));
-    const int seg = p.seg < a.f.L ? p.seg : 0x7fffffff;
-    cudaError_t e;
     if (smem > 48 * 1024) {
-        if ((e = cudaFuncSetAttribute((const void*)diag_bwd_kernel<T, LPC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        if ((e = cudaFuncSetAttribute((const void*)diag_bwd_kernel<T, LPC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+        const cudaError_t e = cudaFuncSetAttribute((const void*)diag_bwd_kernel<T, LPC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
     }
-    if (p.seg < a.f.L) {
-        diag_bwd_kernel<T, LPC, false><<<grid, kThreads, smem, s>>>(a, ws, seg, p.pieces);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    diag_bwd_kernel<T, LPC, true><<<grid, kThreads, smem, s>>>(a, ws, seg, p.pieces);
+    diag_bwd_kernel<T, LPC><<<dim3((unsigned)p.pieces, (unsigned)(p.tiles * a.f.G)), kThreads, smem, s>>>(a, ws, p.seg);
     return cudaGetLastError();
 }
 
@@ -512,7 +437,7 @@ template <typename T>
 cudaError_t launch_t(const DiagBwdArgs& a, const Plan& p, const BwdWs& ws, cudaStream_t s)
 {
     cudaError_t e;
-    switch (bwd_lanes(a.f.N)) {
+    switch (tile_lanes(a.f.N)) {
         case 2: e = launch_lpc<T, 2>(a, p, ws, s); break;
         case 4: e = launch_lpc<T, 4>(a, p, ws, s); break;
         case 8: e = launch_lpc<T, 8>(a, p, ws, s); break;
@@ -534,12 +459,15 @@ cudaError_t launch_diag_scan_bwd(const DiagBwdArgs& a, cudaStream_t s)
     const Plan p = plan_of(a.f.nseq, a.f.L, a.f.E, a.f.N, a.f.G);
     uint8_t* base = static_cast<uint8_t*>(a.f.ws);
     auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
-    const bool cut = p.seg < a.f.L;
-    const BwdWs ws{at(p.ckpt), cut ? at(p.cut) : nullptr, at(p.g), at(p.dA), at(p.dD), at(p.dbias), at(p.bc)};
+    const BwdWs ws{at(p.ckpt), at(p.cut), at(p.gl), at(p.gsdt), at(p.dA), at(p.dD), at(p.dbias), at(p.bc)};
     DiagArgs f = a.f;
-    f.ckpt = ws.ckpt;
     f.ws = ws.cut;
-    cudaError_t e = launch_diag_ckpt(f, p.seg, s);
+    f.dy = a.dy;
+    f.ckpt = ws.ckpt;
+    f.gl = ws.gl;
+    f.gsdt = ws.gsdt;
+    f.bseg = p.seg;
+    cudaError_t e = launch_diag_ckpt(f, s);
     if (e == cudaSuccess) e = a.f.bf16 ? launch_t<__nv_bfloat16>(a, p, ws, s) : launch_t<float>(a, p, ws, s);
     auto sum = [&](const float* part, float* out, int64_t cols) {
         if (e != cudaSuccess) return;
