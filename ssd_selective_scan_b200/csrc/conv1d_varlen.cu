@@ -22,14 +22,33 @@ constexpr int kCpt = 4;      // channels per thread
 constexpr int kPiece = 32;   // rows per piece
 constexpr int kGroup = 8;    // rows loaded together
 
+// A thread's taps and bias.
+template <int K> struct Taps {
+    float w[K][kCpt], b[kCpt];
+    __device__ void load(const float* wp, const float* bp, int c0)
+    {
+        load_taps<K>(wp + (size_t)c0 * K, w);
+#pragma unroll
+        for (int c = 0; c < kCpt; ++c) b[c] = bp ? bp[c0 + c] : 0.0f;
+    }
+    __device__ void apply(const float (&in)[K][kCpt], float (&o)[kCpt]) const
+    {
+        float2 a01 = make_float2(b[0], b[1]), a23 = make_float2(b[2], b[3]);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            a01 = pk_fma(make_float2(w[j][0], w[j][1]), make_float2(in[j][0], in[j][1]), a01);
+            a23 = pk_fma(make_float2(w[j][2], w[j][3]), make_float2(in[j][2], in[j][3]), a23);
+        }
+        o[0] = a01.x * sigmoid_f(a01.x); o[1] = a01.y * sigmoid_f(a01.y);
+        o[2] = a23.x * sigmoid_f(a23.x); o[3] = a23.y * sigmoid_f(a23.y);
+    }
+};
+
+// The rows of one piece for the thread's 4 channels from c0.
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads)
-conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, int64_t os, const float* __restrict__ w,
-                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E)
+__device__ inline void walk_piece(const Piece& p, const T* x, int64_t xs, T* out, int64_t os, const Taps<K>& taps, T* cache,
+                                  const Slots& sl, int E, int c0)
 {
-    const int c0 = (blockIdx.y * kThreads + threadIdx.x) * kCpt;
-    Piece p;
-    if (!find_piece_packed(blockIdx.x, sl, rows, kPiece, K - 2, p) || c0 >= E) return;
     const T* xb = x + c0;
     const bool head = p.t0 == p.s0;
     const int init = head ? sl.init_slot[p.r] : -1;
@@ -38,19 +57,12 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
         return;
     }
 
-    float wt[K][kCpt], bs[kCpt];
-#pragma unroll
-    for (int c = 0; c < kCpt; ++c) bs[c] = bias ? bias[c0 + c] : 0.0f;
-    load_taps<K>(w + (size_t)c0 * K, wt);
-
     // hist[j]: the input K - 1 - j rows before the next one
     float hist[K][kCpt];
     Cache4<T, K> old;
     if (head) {
         if (init >= 0) old.load(cache + ((int64_t)init * E + c0) * K);
-        else
-#pragma unroll
-            for (int i = 0; i < Cache4<T, K>::kWords; ++i) old.w[i] = 0;
+        else old.zero();
 #pragma unroll
         for (int j = 1; j < K; ++j)
 #pragma unroll
@@ -95,7 +107,7 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
 
     // the first row in this piece at which a block ends
     const int64_t flat = sl.slot_of[p.t0];
-    int64_t ends = (int64_t)p.t0 + sl.block - 1 - (flat < 0 ? 0 : flat % sl.block);
+    int64_t ends = (int64_t)p.t0 + sl.block - 1 - block_offset(sl, flat);
     if (flat < 0) flag_invalid(sl.status);
 
     if (head) {
@@ -130,13 +142,8 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
         for (int u = 0; u < kGroup; ++u) {
             if (tb + u < p.t1) {
                 raw[u].get(hist[K - 1]);
-                float2 a01 = make_float2(bs[0], bs[1]), a23 = make_float2(bs[2], bs[3]);
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    a01 = pk_fma(make_float2(wt[j][0], wt[j][1]), make_float2(hist[j][0], hist[j][1]), a01);
-                    a23 = pk_fma(make_float2(wt[j][2], wt[j][3]), make_float2(hist[j][2], hist[j][3]), a23);
-                }
-                const float o[kCpt] = {silu_f(a01.x), silu_f(a01.y), silu_f(a23.x), silu_f(a23.y)};
+                float o[kCpt];
+                taps.apply(hist, o);
                 Row4<T>::store(out + (int64_t)(tb + u) * os + c0, o);
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
@@ -148,12 +155,99 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
 }
 
 template <typename T, int K>
+__global__ void __launch_bounds__(kThreads)
+conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, int64_t os, const float* __restrict__ w,
+                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E)
+{
+    const int c0 = (blockIdx.y * kThreads + threadIdx.x) * kCpt;
+    Piece p;
+    if (!find_piece_packed(blockIdx.x, sl, rows, kPiece, K - 2, p) || c0 >= E) return;
+    Taps<K> taps;
+    taps.load(w, bias, c0);
+    walk_piece<T, K>(p, x, xs, out, os, taps, cache, sl, E, c0);
+}
+
+// Batches of single tokens: a CTA takes SEQS sequences of its channels, so
+// that their taps (64 bytes a thread, against 8 of x) are read once for all
+// and their caches are on the way together.  A sequence of more tokens is
+// walked by the same thread, whole.
+template <typename T, int K, int SEQS>
+__global__ void __launch_bounds__(kThreads)
+conv1d_tokens_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, int64_t os, const float* __restrict__ w,
+                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E)
+{
+    __shared__ int first[SEQS], count[SEQS], init[SEQS], slot[SEQS];
+    if (threadIdx.x < SEQS) {
+        const int r = blockIdx.x * SEQS + threadIdx.x;
+        int n = 0, in = -1, to = -1, s0 = 0;
+        if (r < sl.nseq) {
+            s0 = sl.cu[r];
+            const int s1 = sl.cu[r + 1];
+            in = sl.init_slot[r];
+            if (s0 < 0 || s1 < s0 || s1 > rows || in >= sl.nslots) flag_invalid(sl.status);
+            else n = s1 - s0;
+            if (n == 1) to = slot_at(sl, sl.slot_of[s0]);
+        }
+        first[threadIdx.x] = s0;
+        count[threadIdx.x] = n;
+        init[threadIdx.x] = in;
+        slot[threadIdx.x] = to;
+    }
+    __syncthreads();
+    const int c0 = (blockIdx.y * kThreads + threadIdx.x) * kCpt;
+    if (c0 >= E) return;
+    Cache4<T, K> old[SEQS];
+    Row4<T> in[SEQS];
+#pragma unroll
+    for (int i = 0; i < SEQS; ++i)
+        if (count[i] == 1) {
+            in[i].load(x + (int64_t)first[i] * xs + c0);
+            if (init[i] >= 0) old[i].load(cache + ((int64_t)init[i] * E + c0) * K);
+            else old[i].zero();
+        }
+    Taps<K> taps;
+    taps.load(w, bias, c0);
+#pragma unroll
+    for (int i = 0; i < SEQS; ++i) {
+        if (count[i] == 1) {
+            float v[K][kCpt], o[kCpt];
+            Cache4<T, K> now;
+            in[i].get(v[K - 1]);
+#pragma unroll
+            for (int j = 1; j < K; ++j)
+#pragma unroll
+                for (int c = 0; c < kCpt; ++c) v[j - 1][c] = old[i].get(c, j);
+            taps.apply(v, o);
+            Row4<T>::store(out + (int64_t)first[i] * os + c0, o);
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+#pragma unroll
+                for (int c = 0; c < kCpt; ++c) now.set(c, j, v[j][c]);
+            if (slot[i] >= 0) now.store(cache + ((int64_t)slot[i] * E + c0) * K);
+        } else if (count[i] > 1) {
+            Piece p;
+            p.r = blockIdx.x * SEQS + i;
+            p.t0 = p.s0 = first[i];
+            p.t1 = p.s1 = first[i] + count[i];
+            walk_piece<T, K>(p, x, xs, out, os, taps, cache, sl, E, c0);
+        }
+    }
+}
+
+template <typename T, int K>
 cudaError_t launch_k(const void* x, int64_t xs, void* out, int64_t os, const float* w, const float* bias, void* cache,
                      const SlotArgs& a, int rows, int E, cudaStream_t s)
 {
     const Slots sl{a.cu, a.seq_of, a.slot_of, a.init_slot, a.nseq, a.nslots, a.block, a.status};
     const int per = kThreads * kCpt;
-    const dim3 grid((unsigned)(a.nseq + (rows - 1) / kPiece), (unsigned)((E + per - 1) / per));
+    const unsigned cols = (unsigned)((E + per - 1) / per);
+    if (rows <= 2 * (int64_t)a.nseq) {
+        constexpr int SEQS = sizeof(T) == 2 ? 8 : 4;
+        conv1d_tokens_kernel<T, K, SEQS><<<dim3((unsigned)((a.nseq + SEQS - 1) / SEQS), cols), kThreads, 0, s>>>(
+            static_cast<const T*>(x), xs, static_cast<T*>(out), os, w, bias, static_cast<T*>(cache), sl, rows, E);
+        return cudaGetLastError();
+    }
+    const dim3 grid((unsigned)(a.nseq + (rows - 1) / kPiece), cols);
     conv1d_varlen_kernel<T, K><<<grid, kThreads, 0, s>>>(static_cast<const T*>(x), xs, static_cast<T*>(out), os, w, bias,
                                                          static_cast<T*>(cache), sl, rows, E);
     return cudaGetLastError();

@@ -34,6 +34,11 @@ template <> struct Row4<__nv_bfloat16> {
 template <typename T, int K> struct Cache4 {
     static constexpr int kWords = 4 * K * (int)sizeof(T) / 4;
     uint32_t w[kWords];
+    __device__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
     __device__ void load(const T* p)
     {
 #pragma unroll

@@ -38,6 +38,17 @@ __device__ inline float ex2(float v)
     return r;
 }
 
+// 1 / v on the special-function unit (1 ulp; 1 / inf is 0).
+__device__ inline float rcp(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / (1 + e^-v)
+__device__ inline float sigmoid_f(float v) { return rcp(1.0f + ex2(v * -kLog2e)); }
+
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in [0, 1], with
 // log1p(e) = 2 atanh(w), w = e / (2 + e) <= 1/3, by the series
 // 2 w (1 + w^2/3 + ... + w^12/13): the first term left out is below 2e-8 of
@@ -64,7 +75,7 @@ __device__ inline float2 softplus_pair(float2 v)
 {
     const float2 e = make_float2(ex2(fabsf(v.x) * -kLog2e), ex2(fabsf(v.y) * -kLog2e));
     // (one reciprocal for both would let a NaN of one row into the other)
-    const float2 w = make_float2(__fdividef(e.x, 2.0f + e.x), __fdividef(e.y, 2.0f + e.y));
+    const float2 w = pk_mul(e, make_float2(rcp(2.0f + e.x), rcp(2.0f + e.y)));
     const float2 q = pk_mul(w, w);
     auto both = [](float c) { return make_float2(c, c); };
     float2 p = pk_fma(q, both(1.0f / 13.0f), both(1.0f / 11.0f));
@@ -75,9 +86,6 @@ __device__ inline float2 softplus_pair(float2 v)
     p = pk_fma(q, p, both(1.0f));
     return pk_fma(pk_mul(w, both(2.0f)), p, make_float2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
 }
-
-// 1 / (1 + e^-v)
-__device__ inline float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
 // d SiLU(v) / dv, given sigmoid(v)
 __device__ inline float dsilu_f(float v, float sg) { return sg * fmaf(v, 1.0f - sg, 1.0f); }
@@ -168,15 +176,41 @@ __device__ inline void flag_invalid(int32_t* status)
     if (status) atomicExch(reinterpret_cast<int*>(status), (int)SSD_ERR_INVALID_ARG);
 }
 
-// The slot that token t's block lives in, or -1 (and the status word set) if
+// A flat place in the pool as slot and place in the block.  The 64-bit divide
+// costs a hundred instructions; places below 2^32 take the 32-bit one.
+__device__ inline void split_place(int64_t flat, int block, int64_t& slot, int& off)
+{
+    if ((uint64_t)flat >> 32) {
+        slot = flat / block;
+        off = (int)(flat - slot * block);
+    } else {
+        const uint32_t q = (uint32_t)flat / (uint32_t)block;
+        slot = q;
+        off = (int)((uint32_t)flat - q * (uint32_t)block);
+    }
+}
+
+// The slot that a row's block lives in, or -1 (and the status word set) if
 // the map names none.
 __device__ inline int slot_at(const Slots& s, int64_t flat)
 {
-    if (flat < 0 || flat >= (int64_t)s.nslots * s.block) {
+    int64_t slot;
+    int off;
+    split_place(flat, s.block, slot, off);   // a negative place is beyond any pool
+    if (flat < 0 || slot >= s.nslots) {
         flag_invalid(s.status);
         return -1;
     }
-    return (int)(flat / s.block);
+    return (int)slot;
+}
+
+// The place in its block of a row (0 for a place the map does not name).
+__device__ inline int block_offset(const Slots& s, int64_t flat)
+{
+    int64_t slot;
+    int off;
+    split_place(flat, s.block, slot, off);
+    return flat < 0 ? 0 : off;
 }
 
 // One piece of one sequence: the rows t0 .. t1-1 of sequence r = [s0, s1).

@@ -93,7 +93,7 @@ extern "C" {
 
 size_t ssd_state_map_workspace_bytes(int n)
 {
-    return n < 0 ? 0 : round_up_256(((size_t)kMapWsHeader + n) * 4);
+    return n < 0 ? 0 : ((size_t)kMapWsHeader + n) * 4;
 }
 
 ssd_status_t ssd_state_map(const int32_t* lens, const int32_t* ctx, const int32_t* table, const int32_t* free_list,

@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kOutput && sizeof(T) == 2 ? 
     int64_t keep = 0x7fffffffffffLL;
     if (PACKED && OUT) {
         const int64_t flat = sl.slot_of[p.t0];
-        if (flat >= 0) keep = (int64_t)p.t0 + sl.block - 1 - flat % sl.block;
+        if (flat >= 0) keep = (int64_t)p.t0 + sl.block - 1 - block_offset(sl, flat);
     }
     const int keep_end = min(p.t1, p.s1 - 1);   // the sequence's last state is written behind the walk
     float sdt[2] = {0.0f, 0.0f};

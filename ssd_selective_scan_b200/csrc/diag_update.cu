@@ -4,11 +4,11 @@
 // HBM-bound: 8 bytes of state move per element (4 in, 4 out) for one
 // exponential and four FMAs.  LPC lanes share a channel, 4 states (16 bytes)
 // each, so a warp reads and writes 512 adjacent bytes of a state.  A CTA
-// takes CH = 128 / LPC channels of kUpdRows rows: each thread first issues
-// its kUpdRows state loads (128 bytes in flight per thread), and while those
-// are on their way the CTA forms dt and x = dt u once per (row, channel) and
-// lays them and the rows' B and C out in shared memory, so that the lanes of
-// a channel do not each load and compute them again.  A, D and dt_bias are
+// takes CH = 128 / LPC channels of kUpdRows rows: it looks the rows' slots up
+// once, issues its state loads (kUpdRows x 16 bytes in flight per thread), and
+// while those are on their way forms dt and x = dt u once per (row, channel)
+// and lays them and the rows' B and C out in shared memory, so that the lanes
+// of a channel do not each load and compute them again.  A, D and dt_bias are
 // read once for the rows.  y's sums over a channel's lanes are exchanged for
 // all rows at once, each lane ending with some of the rows.
 #include "diag.cuh"
@@ -39,30 +39,32 @@ __global__ void __launch_bounds__(kUpdThreads) diag_update_kernel(const DiagArgs
     const int i0 = blockIdx.x * ROWS;
 
     // rows -> slots; -1 to a row that is left out
-    int from[ROWS], to[ROWS];
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-        const int i = i0 + k;
-        from[k] = to[k] = -1;
-        if (i >= a.rows) continue;
-        if (!sl.cu) {
-            from[k] = to[k] = i;
-            continue;
+    __shared__ int from[ROWS], to[ROWS];
+    if (tid < ROWS) {
+        const int i = i0 + tid;
+        int f = -1, t = -1;
+        if (i < a.rows) {
+            if (!sl.cu) {
+                f = t = i;
+            } else {
+                const int r = sl.seq_of[i];
+                const int64_t flat = sl.slot_of[i];
+                if (r >= 0) {
+                    const bool sound = r < sl.nseq && sl.cu[r] == i && sl.cu[r + 1] == i + 1;
+                    const int init = sound ? sl.init_slot[r] : 0;
+                    if (!sound || init >= sl.nslots) {
+                        flag_invalid(sl.status);
+                    } else {
+                        t = slot_at(sl, flat);
+                        f = init;
+                    }
+                }
+            }
         }
-        const int r = sl.seq_of[i];
-        if (r < 0) continue;
-        if (r >= sl.nseq || sl.cu[r] != i || sl.cu[r + 1] != i + 1) {
-            flag_invalid(sl.status);
-            continue;
-        }
-        const int init = sl.init_slot[r];
-        if (init >= sl.nslots) {
-            flag_invalid(sl.status);
-            continue;
-        }
-        to[k] = slot_at(sl, sl.slot_of[i]);
-        from[k] = init;
+        from[tid] = f;
+        to[tid] = t;
     }
+    __syncthreads();
     float4 st[ROWS];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
@@ -118,14 +120,7 @@ __global__ void __launch_bounds__(kUpdThreads) diag_update_kernel(const DiagArgs
     for (int k = tid; k < ROWS * CH; k += kUpdThreads) {
         const int row = k / CH, c = k % CH;
         const int64_t i = i0 + row;
-        bool out = i < a.rows && e0 + c < e_end;
-        if (out && sl.cu) {
-            // as above, by row
-            const int r = sl.seq_of[i];
-            out = r >= 0 && r < sl.nseq && sl.cu[r] == i && sl.cu[r + 1] == i + 1 && sl.init_slot[r] < sl.nslots &&
-                  slot_at(sl, sl.slot_of[i]) >= 0;
-        }
-        if (!out) continue;
+        if (to[row] < 0 || e0 + c >= e_end) continue;
         float y = dx[row][c].x;
         if (a.D) y = fmaf(a.D[e0 + c], ld_f(static_cast<const T*>(a.u) + i * a.us + e0 + c), y);
         if (a.z) {

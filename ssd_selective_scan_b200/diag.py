@@ -174,21 +174,33 @@ def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_l
         raise ValueError("out was made for another block size")
     with _On(lens, stream) as on:
         dev = on.device
+        scratch = 64 + n      # the workspace, in int32
         if out is None:
-            # one allocation for the int32 parts; seq_of and pos_of on 16 bytes
+            # one allocation for the int32 parts (seq_of and pos_of on 16
+            # bytes) and the workspace
             n4, T4 = (n + 4) // 4 * 4, (T + 3) // 4 * 4
-            cu, _, seq, _, pos, _, init, _, tab, head = on.empty(n4 + 2 * T4 + n4 + n * mb + 1, i32).split_with_sizes(
-                (n + 1, n4 - n - 1, T, T4 - T, T, T4 - T, n, n4 - n, n * mb, 1))
+            parts = on.empty(n4 + 2 * T4 + n4 + n * mb + 1 + (0 if workspace is not None else scratch), i32)
+            cu, _, seq, _, pos, _, init, _, tab, head, _ = parts.split_with_sizes(
+                (n + 1, n4 - n - 1, T, T4 - T, T, T4 - T, n, n4 - n, n * mb, 1, 0 if workspace is not None else scratch))
             out = StateMap(cu, seq, pos, on.empty(T, torch.int64), init, tab.view(n, mb), head, block_tokens)
-        cu, seq, slot, init, _ = _map(out, T, dev)
-        pos = _dense(out.pos_of, "pos_of", i32, (T,), dev)
-        wp, wb = on.workspace(workspace, int(libssd.ssd_state_map_workspace_bytes(n)))
+            at = parts.data_ptr()
+            ptrs = (at, at + 4 * n4, at + 4 * (n4 + T4), out.slot_of.data_ptr(), at + 4 * (n4 + 2 * T4), at + 4 * (2 * n4 + 2 * T4),
+                    at + 4 * (2 * n4 + 2 * T4 + n * mb))
+            if workspace is None:
+                wp, wb = ptrs[-1] + 4, 4 * scratch
+        else:
+            cu, seq, slot, init, _ = _map(out, T, dev)
+            ptrs = (cu, seq, _dense(out.pos_of, "pos_of", i32, (T,), dev), slot, init, _dense(out.table, "out.table", i32, (n, mb), dev),
+                    _dense(out.free_head, "out.free_head", i32, (1,), dev))
+            if workspace is None:
+                wp, wb = on.workspace(None, 4 * scratch)
+        if workspace is not None:
+            wp, wb = on.workspace(workspace, 4 * scratch)
+        nfree = free_list.numel()
         st = libssd.ssd_state_map(
             _dense(lens, "lens", i32, (n,), dev), _dense(ctx, "ctx", i32, (n,), dev), _dense(table, "table", i32, (n, mb), dev),
-            _dense(free_list, "free_list", i32, (free_list.numel(),), dev), _dense(free_head, "free_head", i32, (1,), dev),
-            n, mb, free_list.numel(), T, block_tokens, nslots, cu, seq, pos, slot, init,
-            _dense(out.table, "out.table", i32, (n, mb), dev), _dense(out.free_head, "out.free_head", i32, (1,), dev), wp, wb,
-            _status(status, on), on.handle)
+            _dense(free_list, "free_list", i32, (nfree,), dev), _dense(free_head, "free_head", i32, (1,), dev),
+            n, mb, nfree, T, block_tokens, nslots, *ptrs, wp, wb, _status(status, on), on.handle)
         libssd.check("ssd_state_map", st)
     return out
 

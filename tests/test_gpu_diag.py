@@ -148,6 +148,8 @@ CONV_BATCHES = {
     "block_of_two": ([37, 66], [1, 0], 2),
     "odd_blocks": ([100, 29, 31], [3, 0, 50], 7),
     "in_one_block": ([100, 200, 1], [30, 0, 7], 100000),
+    # fewer rows than requests: single tokens, none, and a few longer ones
+    "mostly_empty": ([0] * 11 + [1, 0, 7, 0, 1, 1] + [0] * 9 + [2] + [0] * 6, [(5 * i) % 13 for i in range(33)], 4),
 }
 
 

@@ -174,6 +174,11 @@ def test_conv_bwd(b, L, E, full, k, dtype):
         assert r["dbias"] is None and r["dconv_state"] is None
 
 
+def test_conv_bwd_long_tiles():
+    """Enough channels and rows for the 256-row tiles, the last one short."""
+    test_conv_bwd(10, 270, 7608, True, 4, BF16)
+
+
 def test_conv_bwd_empty():
     w = torch.randn(16, 4, device="cuda")
     x = torch.zeros(2, 0, 16, device="cuda")
