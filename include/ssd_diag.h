@@ -189,7 +189,7 @@ SSD_API ssd_status_t ssd_diag_scan_fwd_varlen(const void* u, int64_t u_stride, c
  *   dB, dC [b][L][G][N] dtype, written (summed over each group's channels)
  *   dA [E][N], dD, ddt_bias [E] float32, written (summed over the batch)
  *   dinit  [b][E][N] float32, written, may be NULL (not wanted)
- *   workspace  ssd_diag_scan_bwd_workspace_bytes(...) bytes: states every 8
+ *   workspace  ssd_diag_scan_bwd_workspace_bytes(...) bytes: states every 4
  *          tokens and partial sums, no initial contents
  * Deterministic: no atomics.  b == 0 or L == 0 zeroes dA, dD and ddt_bias
  * and copies dfinal (or zeros) into dinit.

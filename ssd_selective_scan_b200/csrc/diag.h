@@ -58,6 +58,10 @@ struct DiagArgs {
     bool longest_first = false;   // packed: sequences are taken up by length
     bool bc_aligned = false;   // every 4 elements of a B or C row are aligned to their size
 };
+inline bool bc_aligned(const DiagArgs& a, size_t elem)
+{
+    return a.bcs % 4 == 0 && reinterpret_cast<uintptr_t>(a.B) % (4 * elem) == 0 && reinterpret_cast<uintptr_t>(a.C) % (4 * elem) == 0;
+}
 size_t diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G);
 cudaError_t launch_diag_scan(const DiagArgs& a, cudaStream_t s);
 cudaError_t launch_diag_update(const DiagArgs& a, cudaStream_t s);
@@ -69,7 +73,7 @@ cudaError_t launch_diag_update(const DiagArgs& a, cudaStream_t s);
 // own rows, to a.gl [E][N], and the sum of its dt, to a.gsdt [E].  The walk is
 // itself cut every diag_ckpt_rows(...) rows (L: not at all), with
 // diag_cut_bytes(...) of workspace at a.ws.
-constexpr int kDiagCkpt = 8;
+constexpr int kDiagCkpt = 4;
 #ifdef __CUDACC__
 __host__ __device__
 #endif

@@ -104,7 +104,7 @@ inline size_t cut_ws_bytes(int nseq, int64_t pieces, int E, int N) { return ((si
 
 // CUT: the pieces' states are in the workspace.
 template <typename T, int LPC, bool PACKED, Mode MODE, bool CUT>
-__global__ void __launch_bounds__(kThreads, MODE == kOutput && sizeof(T) == 2 ? 5 : 4) diag_scan_kernel(const DiagArgs a, int seg, int64_t pieces)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) diag_scan_kernel(const DiagArgs a, int seg, int64_t pieces)
 {
     using TL = DiagTile<LPC, kWarps>;
     constexpr bool OUT = MODE == kOutput, WITH_C = OUT || MODE == kCkptG;
@@ -378,6 +378,10 @@ __global__ void __launch_bounds__(kThreads, MODE == kOutput && sizeof(T) == 2 ? 
         }
     };
     restart();
+    // kept states: every 4 rows, and pieces start at multiples of that
+    static_assert(kDiagCkpt == 4, "a state is kept before each walk of 4 rows");
+    [[maybe_unused]] float* kept = a.ckpt + ((int64_t)p.r * ckpts_of(a.L) + (p.t0 - p.s0) / kDiagCkpt) * st_all;
+    [[maybe_unused]] int piece_end = MODE == kCkptG ? min(p.t0 + a.bseg, p.s1) : 0;
 
     for (int it = 0; it < ntile; ++it) {
         const int buf = it & 1, t = p.t0 + it * TT;
@@ -387,11 +391,10 @@ __global__ void __launch_bounds__(kThreads, MODE == kOutput && sizeof(T) == 2 ? 
         auto walk4 = [&](int gr, auto keeps) {
             constexpr bool KEEPS = decltype(keeps)::value;
             if constexpr (MODE == kCkpt || MODE == kCkptG) {
-                const int row = t + 4 * gr - p.s0;   // pieces start at multiples of kDiagCkpt
-                if (row % kDiagCkpt == 0)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (live[j]) put4(a.ckpt + ((int64_t)p.r * ckpts_of(a.L) + row / kDiagCkpt) * st_all + st[j], h[j]);
+                for (int j = 0; j < 2; ++j)
+                    if (live[j]) put4(kept + st[j], h[j]);
+                kept += st_all;
             }
             [[maybe_unused]] float2 acc[2][2];
 #pragma unroll
@@ -404,14 +407,14 @@ __global__ void __launch_bounds__(kThreads, MODE == kOutput && sizeof(T) == 2 ? 
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float4 d = sm.dx[buf][pr][TL::col16(cl[j], pr)];
-                    const float2 dd = make_float2(d.x, d.y), xx = make_float2(d.z, d.w);
-                    float2 pp;
+                    const float2 xx = make_float2(d.z, d.w);
+                    [[maybe_unused]] float2 pp;
                     if constexpr (MODE == kCkptG) pp = sm.p[buf][pr][TL::col8(cl[j], pr)];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const float2 b2 = n & 1 ? make_float2(bb[n >> 1].z, bb[n >> 1].w) : make_float2(bb[n >> 1].x, bb[n >> 1].y);
-                        const float2 e = pk_mul(make_float2(A2[j][n], A2[j][n]), dd);
-                        const float a0 = ex2(e.x), a1 = ex2(e.y);
+                        // (scalar: a pair of A would have to be copied together)
+                        const float a0 = ex2(A2[j][n] * d.x), a1 = ex2(A2[j][n] * d.y);
                         const float2 xb = pk_mul(xx, b2);
                         h0[j][n] = fmaf(a0, h[j][n], xb.x);
                         h[j][n] = fmaf(a1, h0[j][n], xb.y);
@@ -471,9 +474,10 @@ __global__ void __launch_bounds__(kThreads, MODE == kOutput && sizeof(T) == 2 ? 
             }
             if constexpr (MODE == kCkptG) {
                 // a backward piece ends behind these rows, or with the sequence
-                const int row = t + 4 * gr + 4 - p.s0;
-                if (row % a.bseg == 0 || row >= p.s1 - p.s0) {
-                    const int64_t i = (int64_t)p.r * pieces_per(a.L, a.bseg) + (row - 1) / a.bseg;
+                const int row = t + 4 * gr + 4;
+                if (row >= piece_end) {
+                    const int64_t i = (int64_t)p.r * pieces_per(a.L, a.bseg) + (piece_end - 1 - p.s0) / a.bseg;
+                    piece_end = min(piece_end + a.bseg, p.s1);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         if (live[j]) {

@@ -10,43 +10,55 @@
 //   dD = sum_t u_t p_t,   dz_t = dy_t (sum_n h_t C_t + D u_t) SiLU'(z_t).
 // The products need h and g of the same row, one recurrence running forward
 // and one backward.  So a first kernel walks forward and leaves the state
-// before every 8th row (8 bytes per token and channel at N = 16); this one
-// walks the rows from the end, 8 at a time: forward from the kept state with
-// the 8 decays and states in registers, then back over them.
+// before every 4th row (16 bytes per token and channel at N = 16; HBM has room
+// for them, and keeping every 8th costs the walk of 4 rows in 8 once more);
+// this one walks the rows from the end, 4 at a time: forward from the kept
+// state, with a and a h of the 4 rows in registers (w_t = g_t (a_t h_{t-1}),
+// so h itself is not needed after its products with C and p), then back.  Rows
+// lie in pairs, as in the forward scan, for the packed instructions.
+//
+// Rows in pieces.  The kernel's time is that of its fullest SM, and a piece's
+// walk needs G behind it.  The forward walk has the decays at hand, so it also
+// leaves each piece's part of G at its start, sum_t (a_s .. a_t) C_t p_t, for
+// two more products per element; folded over the pieces behind, that is the
+// piece's G, and the rows can be cut as finely as balances the device.
 //
 // Sums go both ways, over states (gB, w A, and y for dz) and over channels
-// (dB, dC), so a thread owns a patch of 2 channels x 4 states: both sums
-// begin in registers, where a patch of one channel would send twice the
-// values through the channel sum.  LPC lanes hold a channel's states, the
-// other lanes of the warp other channels, and each sum is finished by an
-// exchange that halves the values a lane keeps with every step (7 shuffles
-// for 8 channel sums over 8 lanes, 3 for 4 state sums over 4).  The 4 warps'
-// channel sums meet in shared memory, the CTAs' in the workspace, where a
-// last kernel adds them in a fixed order: no atomics, the same bits each run.
-// dA, dD and ddt_bias are summed the same way per piece.
+// (dB, dC), so a thread owns a patch of 2 channels x 4 states (diag_tile.cuh):
+// both sums begin in registers.  Each is finished by an exchange that halves
+// the values a lane keeps with every step, and where it can without a
+// selection: a lane's slots hold its states in an order of its own (slot k is
+// state k ^ m, m from the lane's channel number), so that what it keeps and
+// what it sends are the same slots in every lane.  B and C lie in shared
+// memory in all four orders.  The warps' channel sums meet in shared memory,
+// the CTAs' in the workspace, where a last kernel adds them in a fixed order:
+// no atomics, the same bits each run.  dA, dD and ddt_bias are summed the same
+// way per piece.
 //
-// u, dt_raw, dy and z are copied to shared memory one tile ahead (cp.async);
-// dt, x and p are formed from them once per token and channel, and the state
-// sums return through the same places to the threads that write du, ddt_raw
-// and dz in 16-byte vectors.
+// The walk is four fifths of the work here, so all four warps walk (half of
+// them feeding the others, as in the forward scan, took 1700 us where this
+// takes the time below).  Between two tiles' walks one half of the CTA lays
+// out the next tile (u, dt_raw, dy and z by cp.async a tile ahead; dt, x and p
+// formed once per token and channel) while the other finishes du, ddt_raw and
+// dz of the last one from its sums, in 16-byte vectors.
 //
-// Bound by instruction issue, not by HBM: per token, channel and state 2
-// exponentials (one per walk) and about 20 other instructions.
+// Bound by instruction issue, not by HBM.
 #include "diag_tile.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kHalf = kThreads / 2;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T, int LPC> struct Smem {
     using TL = DiagTile<LPC, kWarps>;
-    float4 tile[TL::TT][TL::CH];              // dt, x -> gB, p, w A
-    float ysum[TL::TT][TL::CH];
-    float4 B[TL::TT][LPC], C[TL::TT][LPC];
-    float2 red[kWarps][TL::TT][TL::NP];       // dB, dC of each warp's channels
+    static constexpr int PAIRS = TL::TT / 2;
+    float4 tile[2][PAIRS][TL::CH];            // dt, dt', x, x' of two rows
+    float2 p[2][PAIRS][TL::CH];
+    float4 B[PAIRS][2][4][LPC], C[PAIRS][2][4][LPC];   // [half][order][lane]: b0, b0', b1, b1'; b2, ..
     T raw[2][4][TL::TT][TL::CH];              // u, dt_raw, dy, z
 };
 
@@ -55,283 +67,420 @@ struct BwdWs {
     float *ckpt, *cut, *gl, *gsdt, *dA, *dD, *dbias, *bc;
 };
 
-template <typename T, int LPC>
-__global__ void __launch_bounds__(kThreads) diag_bwd_kernel(const DiagBwdArgs ba, const BwdWs ws, int seg)
+// A thread's 4 states in the order of its slots (and back: the order is its
+// own inverse).
+__device__ inline float4 order4(float4 v, int m)
 {
-    using TL = DiagTile<LPC, kWarps>;
-    constexpr int NL = TL::NL, TT = TL::TT, VPR = TL::VPR, NP = TL::NP, NBC = TL::NBC;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<T, LPC>& sm = *reinterpret_cast<Smem<T, LPC>*>(smem_raw);
-    const DiagArgs& a = ba.f;
+    if (m & 2) v = make_float4(v.z, v.w, v.x, v.y);
+    if (m & 1) v = make_float4(v.y, v.x, v.w, v.z);
+    return v;
+}
 
-    Piece p;
-    find_piece_dense(blockIdx.x, a.L, seg, p);
+// keep + the partner's send, d lanes away
+__device__ inline float ex(float keep, float send, int d) { return keep + __shfl_xor_sync(0xffffffffu, send, d); }
+__device__ inline float2 ex(float2 keep, float2 send, int d) { return make_float2(ex(keep.x, send.x, d), ex(keep.y, send.y, d)); }
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int q = lane % LPC, cg = lane / LPC;
-    const ChannelTile ct(a.E, a.G, TL::CH, blockIdx.y);
-    const int e0 = ct.e0, e_end = ct.e_end;
-    const int n0 = 4 * q;
-    const int64_t st_all = (int64_t)a.E * a.N;
-    int cl[2], col[2];
-    int64_t st[2];
-    bool live[2];
-    float2 A2[2][2];
+// Sums over a warp's channel lanes of a pair of rows' 4 slots: slots 0 and 2,
+// then slot 0, are kept; of 8 lanes and more, a row; put(row, slot, sum).
+template <int LPC, typename PUT>
+__device__ inline void channel_sum(const float2 (&s)[4], int cg, PUT put)
+{
+    constexpr int NL = 32 / LPC;
+    float2 v = ex(s[0], s[1], LPC);
+    const float2 v2 = ex(s[2], s[3], LPC);
+    if constexpr (NL == 2) {
+        put(0, 0, v.x);
+        put(1, 0, v.y);
+        put(0, 2, v2.x);
+        put(1, 2, v2.y);
+    } else {
+        v = ex(v, v2, 2 * LPC);
+        if constexpr (NL == 4) {
+            put(0, 0, v.x);
+            put(1, 0, v.y);
+        } else {
+            const int up = cg >> 2 & 1;
+            float one = ex(up ? v.y : v.x, up ? v.x : v.y, 4 * LPC);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        cl[j] = TL::channel(warp, lane, j);
-        col[j] = TL::col16(cl[j], 0);
-        live[j] = e0 + cl[j] < e_end && n0 < a.N;
-        st[j] = (int64_t)(e0 + cl[j]) * a.N + n0;
-        A2[j][0] = A2[j][1] = make_float2(0.0f, 0.0f);
-        if (live[j]) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + st[j]));
-            A2[j][0] = make_float2(v.x * kLog2e, v.y * kLog2e);
-            A2[j][1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+            for (int o = 8; o < NL; o <<= 1) one = ex(one, one, o * LPC);
+            put(up, 0, one);
         }
     }
+}
 
-    // G behind the piece's last row: dfinal, folded over the pieces behind
-    float2 G[2][2], dA[2][2];
+template <typename T, int LPC>
+__global__ void __launch_bounds__(kThreads, 3) diag_bwd_kernel(const DiagBwdArgs ba, const BwdWs ws, int seg)
+{
+    using TL = DiagTile<LPC, kWarps>;
+    constexpr int NL = TL::NL, CH = TL::CH, NP = TL::NP, VPR = TL::VPR, TT = TL::TT, PAIRS = TT / 2;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Smem<T, LPC>& sm = *reinterpret_cast<Smem<T, LPC>*>(smem_raw);
+    // the walk's results: objects of their own, so that its reads of other
+    // rows need not wait for these writes
+    __shared__ __align__(16) float gb_sum[TT][CH], wa_sum[TT][CH], y_sum[TT][CH];
+    __shared__ float2 red[kWarps][TT][NP];      // dB, dC of each warp's channels
+    __shared__ float2 tails[8][PAIRS * VPR];    // dD, ddt_bias of the piece, by pair of rows and vector
+    const DiagArgs& a = ba.f;
+
+    const int ntiles = channel_tiles(a.E, a.G, CH) * a.G;
+    const int piece = (int)(blockIdx.x / ntiles), ytile = blockIdx.x - piece * ntiles;
+    Piece p;
+    find_piece_dense(piece, a.L, seg, p);
+    const ChannelTile ct(a.E, a.G, CH, ytile);
+    const int e0 = ct.e0, e_end = ct.e_end;
+    const int64_t st_all = (int64_t)a.E * a.N;
+    const int ntile = (p.t1 - p.t0 + TT - 1) / TT;
+    const bool gated = a.z != nullptr;
+    const int tid = threadIdx.x;
+    const bool lower = tid < kHalf;
+    // tile w of the walk, which goes from the end
+    auto tile_row = [&](int w) { return p.t0 + (ntile - 1 - w) * TT; };
+
+    // Each half of the CTA shares the tile out: item i is vector i % VPR of
+    // the pair of rows i / VPR.
+    constexpr int ITEMS = PAIRS * VPR, PER = (ITEMS + kHalf - 1) / kHalf;
+    const int half_id = lower ? tid : tid - kHalf;
+    auto fetch = [&](int w) {      // the lower half: tile w, on its way
+        auto& raw = sm.raw[w & 1];
+        if (w < ntile)
+#pragma unroll
+            for (int k = 0; k < 2 * PER; ++k) {
+                const int i = half_id + (k >> 1) * kHalf, r = 2 * (i / VPR) + (k & 1), c = 8 * (i % VPR);
+                const int64_t row = tile_row(w) + r;
+                if (i < ITEMS && row < p.t1 && e0 + c < e_end) {
+                    cp_row8(&raw[0][r][c], static_cast<const T*>(a.u) + row * a.us + e0 + c);
+                    cp_row8(&raw[1][r][c], static_cast<const T*>(a.dt) + row * a.dts + e0 + c);
+                    cp_row8(&raw[2][r][c], static_cast<const T*>(ba.dy) + row * a.E + e0 + c);
+                    if (gated) cp_row8(&raw[3][r][c], static_cast<const T*>(a.z) + row * a.zs + e0 + c);
+                }
+            }
+        cp_commit();
+    };
+    auto lay_out = [&](int w) {    // the lower half
+        cp_wait_all();             // a thread reads back what it copied itself
+        auto& raw = sm.raw[w & 1];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = half_id + k * kHalf, pr = i / VPR, c = 8 * (i % VPR);
+            if (i >= ITEMS) break;
+            const bool in = e0 + c < e_end;   // rows and channels outside change nothing
+            const bool ok0 = in && tile_row(w) + 2 * pr < p.t1, ok1 = in && tile_row(w) + 2 * pr + 1 < p.t1;
+            const Raw8<T> u0 = smem_row8(&raw[0][2 * pr][c]), u1 = smem_row8(&raw[0][2 * pr + 1][c]);
+            const Raw8<T> v0 = smem_row8(&raw[1][2 * pr][c]), v1 = smem_row8(&raw[1][2 * pr + 1][c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float bias = in && a.dt_bias ? __ldg(a.dt_bias + e0 + c + j) : 0.0f;
+                const float2 dt = softplus_pair(make_float2(v0.get(j) + bias, v1.get(j) + bias));
+                sm.tile[w & 1][pr][TL::col16(c + j, pr)] =
+                    make_float4(ok0 ? dt.x : 0.0f, ok1 ? dt.y : 0.0f, ok0 ? dt.x * u0.get(j) : 0.0f, ok1 ? dt.y * u1.get(j) : 0.0f);
+            }
+            const Raw8<T> g0 = smem_row8(&raw[2][2 * pr][c]), g1 = smem_row8(&raw[2][2 * pr + 1][c]);
+            const Raw8<T> z0 = smem_row8(&raw[3][2 * pr][c]), z1 = smem_row8(&raw[3][2 * pr + 1][c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 g = make_float2(g0.get(j), g1.get(j));
+                if (gated) {
+                    g.x *= z0.get(j) * sigmoid_f(z0.get(j));
+                    g.y *= z1.get(j) * sigmoid_f(z1.get(j));
+                }
+                sm.p[w & 1][pr][TL::col8(c + j, pr)] = make_float2(ok0 ? g.x : 0.0f, ok1 ? g.y : 0.0f);
+            }
+        }
+    };
+    // B and C: quads of states of pairs of rows, to the upper half
+    constexpr int QUADS = (PAIRS * LPC + kHalf - 1) / kHalf;
+    float bv[QUADS][2][4], cv[QUADS][2][4];
+    auto fetch_bc = [&](int w) {
+        const T* Bp = static_cast<const T*>(a.B) + (int64_t)ct.group * a.N;
+        const T* Cp = static_cast<const T*>(a.C) + (int64_t)ct.group * a.N;
+#pragma unroll
+        for (int k = 0; k < QUADS; ++k) {
+            const int at = half_id + k * kHalf, n = 4 * (at % LPC);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t row = tile_row(w) + 2 * (at / LPC) + h;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bv[k][h][i] = cv[k][h][i] = 0.0f;
+                if (w < ntile && at < PAIRS * LPC && row < p.t1 && n < a.N) {
+                    load4(Bp + row * a.bcs + n, a.bc_aligned, bv[k][h]);
+                    load4(Cp + row * a.bcs + n, a.bc_aligned, cv[k][h]);
+                }
+            }
+        }
+    };
+    auto lay_out_bc = [&] {
+#pragma unroll
+        for (int k = 0; k < QUADS; ++k) {
+            const int at = half_id + k * kHalf, pr = at / LPC, q = at % LPC;
+            if (at < PAIRS * LPC)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    sm.B[pr][0][m][q] = make_float4(bv[k][0][m], bv[k][1][m], bv[k][0][1 ^ m], bv[k][1][1 ^ m]);
+                    sm.B[pr][1][m][q] = make_float4(bv[k][0][2 ^ m], bv[k][1][2 ^ m], bv[k][0][3 ^ m], bv[k][1][3 ^ m]);
+                    sm.C[pr][0][m][q] = make_float4(cv[k][0][m], cv[k][1][m], cv[k][0][1 ^ m], cv[k][1][1 ^ m]);
+                    sm.C[pr][1][m][q] = make_float4(cv[k][0][2 ^ m], cv[k][1][2 ^ m], cv[k][0][3 ^ m], cv[k][1][3 ^ m]);
+                }
+        }
+    };
+    auto finish = [&](int w) {     // the upper half
+        const int t = tile_row(w);
+        auto& raw = sm.raw[w & 1];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = half_id + k * kHalf, pr = i / VPR, c = 8 * (i % VPR);
+            if (i >= ITEMS || t + 2 * pr >= p.t1 || e0 + c >= e_end) break;
+            float dt[2][8], pv[2][8], sD[8], sb[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 d = *reinterpret_cast<const float2*>(&sm.tile[w & 1][pr][TL::col16(c + j, pr)]);
+                const float2 g = sm.p[w & 1][pr][TL::col8(c + j, pr)];
+                dt[0][j] = d.x; dt[1][j] = d.y;
+                pv[0][j] = g.x; pv[1][j] = g.y;
+                sD[j] = sb[j] = 0.0f;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 2 * pr + h;
+                if (t + r >= p.t1) break;
+                const int64_t o = (int64_t)(t + r) * a.E + e0 + c;
+                const Raw8<T> u = smem_row8(&raw[0][r][c]), v = smem_row8(&raw[1][r][c]);
+                float gb[8], wa[8], out[8], Dv[8];
+                *reinterpret_cast<float4*>(gb) = *reinterpret_cast<const float4*>(&gb_sum[r][c]);
+                *reinterpret_cast<float4*>(gb + 4) = *reinterpret_cast<const float4*>(&gb_sum[r][c + 4]);
+                *reinterpret_cast<float4*>(wa) = *reinterpret_cast<const float4*>(&wa_sum[r][c]);
+                *reinterpret_cast<float4*>(wa + 4) = *reinterpret_cast<const float4*>(&wa_sum[r][c + 4]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    Dv[j] = a.D ? __ldg(a.D + e0 + c + j) : 0.0f;
+                    const float bias = a.dt_bias ? __ldg(a.dt_bias + e0 + c + j) : 0.0f;
+                    const float uv = u.get(j);
+                    out[j] = fmaf(Dv[j], pv[h][j], dt[h][j] * gb[j]);
+                    wa[j] = fmaf(uv, gb[j], wa[j] * kLn2) * sigmoid_f(v.get(j) + bias);
+                    sD[j] = fmaf(uv, pv[h][j], sD[j]);
+                    sb[j] += wa[j];
+                }
+                Raw8<T>::store(static_cast<T*>(ba.du) + o, out);
+                Raw8<T>::store(static_cast<T*>(ba.ddt) + o, wa);
+                if (gated) {
+                    const Raw8<T> dy = smem_row8(&raw[2][r][c]), z = smem_row8(&raw[3][r][c]);
+                    *reinterpret_cast<float4*>(gb) = *reinterpret_cast<const float4*>(&y_sum[r][c]);
+                    *reinterpret_cast<float4*>(gb + 4) = *reinterpret_cast<const float4*>(&y_sum[r][c + 4]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float zv = z.get(j);
+                        out[j] = dy.get(j) * fmaf(Dv[j], u.get(j), gb[j]) * dsilu_f(zv, sigmoid_f(zv));
+                    }
+                    Raw8<T>::store(static_cast<T*>(ba.dz) + o, out);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 s = tails[j][i];   // this thread's alone
+                s.x += sD[j];
+                s.y += sb[j];
+                tails[j][i] = s;
+            }
+        }
+    };
+    auto sum_warps = [&](int w) {  // the lower half
+        const int t = tile_row(w), rows = min(TT, p.t1 - t);
+        for (int k = half_id; k < rows * NP; k += kHalf) {
+            const int row = k / NP, n = k % NP;
+            if (n < a.N) {
+                float2 s = red[0][row][n];
+#pragma unroll
+                for (int i = 1; i < kWarps; ++i) {
+                    s.x += red[i][row][n].x;
+                    s.y += red[i][row][n].y;
+                }
+                reinterpret_cast<float2*>(ws.bc)[((int64_t)ytile * a.rows + t + row) * a.N + n] = s;
+            }
+        }
+    };
+    for (int i = tid; i < 8 * ITEMS; i += kThreads) tails[i / ITEMS][i % ITEMS] = make_float2(0.0f, 0.0f);
+    if (lower) fetch(0);
+    else fetch_bc(0);
+
+    const int lane = tid & 31, warp = tid >> 5;
+    const int q = lane % LPC, cg = lane / LPC, n0 = 4 * q;
+    const int m = cg & (NL >= 4 ? 3 : 1);          // the order of this lane's slots
+    int cl[2];
+    int64_t st[2];
+    bool live[2];
+    float A2[2][4], G[2][4];
+    float2 dA[2][4];                               // of the pairs' first and second rows
+    auto put4 = [&](float4 v, float (&o)[4]) {
+        v = order4(v, m);
+        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    };
     const int64_t last = p.first + pieces_per(a.L, seg) - 1;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        G[j][0] = G[j][1] = dA[j][0] = dA[j][1] = make_float2(0.0f, 0.0f);
-        if (!live[j]) continue;
-        if (ba.dfinal) {
-            const float4 v = *reinterpret_cast<const float4*>(ba.dfinal + p.r * st_all + st[j]);
-            G[j][0] = make_float2(v.x, v.y);
-            G[j][1] = make_float2(v.z, v.w);
+        cl[j] = TL::channel(warp, lane, j);
+        live[j] = e0 + cl[j] < e_end && n0 < a.N;
+        st[j] = (int64_t)(e0 + cl[j]) * a.N + n0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            A2[j][k] = G[j][k] = 0.0f;
+            dA[j][k] = make_float2(0.0f, 0.0f);
         }
+        if (!live[j]) continue;
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + st[j]));
+        put4(make_float4(v.x * kLog2e, v.y * kLog2e, v.z * kLog2e, v.w * kLog2e), A2[j]);
+        // G behind the piece's last row: dfinal, folded over the pieces behind
+        if (ba.dfinal) put4(*reinterpret_cast<const float4*>(ba.dfinal + p.r * st_all + st[j]), G[j]);
         for (int64_t i = last; i > p.idx; --i) {
             const float sdt = ws.gsdt[i * a.E + e0 + cl[j]];
-            const float4 v = *reinterpret_cast<const float4*>(ws.gl + i * st_all + st[j]);
-            G[j][0].x = fmaf(ex2(A2[j][0].x * sdt), G[j][0].x, v.x);
-            G[j][0].y = fmaf(ex2(A2[j][0].y * sdt), G[j][0].y, v.y);
-            G[j][1].x = fmaf(ex2(A2[j][1].x * sdt), G[j][1].x, v.z);
-            G[j][1].y = fmaf(ex2(A2[j][1].y * sdt), G[j][1].y, v.w);
+            float g[4];
+            put4(*reinterpret_cast<const float4*>(ws.gl + i * st_all + st[j]), g);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) G[j][k] = fmaf(ex2(A2[j][k] * sdt), G[j][k], g[k]);
         }
     }
-
-    // loading: vector sv of row sr of each tile
-    const int sr = tid / VPR, sv = tid % VPR;
-    const int ev = e0 + 8 * sv;
-    const bool loads = tid < TL::NVEC && ev < e_end;
-    float Dv[8], bias[8], dDs[8], dbs[8];
+    // the state before group g of 4 rows, counted from the piece's start
+    const int64_t ck0 = (int64_t)p.r * ckpts_of(a.L) + (p.t0 - p.s0) / kDiagCkpt;
+    float4 kept[2];
+    auto fetch_kept = [&](int g) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        Dv[j] = loads && a.D ? a.D[ev + j] : 0.0f;
-        bias[j] = loads && a.dt_bias ? a.dt_bias[ev + j] : 0.0f;
-        dDs[j] = dbs[j] = 0.0f;
-    }
-    const T* Bp = static_cast<const T*>(a.B) + (int64_t)ct.group * a.N;
-    const T* Cp = static_cast<const T*>(a.C) + (int64_t)ct.group * a.N;
-    const bool gated = a.z != nullptr;
-
-    auto fetch = [&](int t, int buf) {
-        const int64_t row = t + sr;
-        if (loads && row < p.t1) {
-            cp_row8(&sm.raw[buf][0][sr][8 * sv], static_cast<const T*>(a.u) + row * a.us + ev);
-            cp_row8(&sm.raw[buf][1][sr][8 * sv], static_cast<const T*>(a.dt) + row * a.dts + ev);
-            cp_row8(&sm.raw[buf][2][sr][8 * sv], static_cast<const T*>(ba.dy) + row * a.E + ev);
-            if (gated) cp_row8(&sm.raw[buf][3][sr][8 * sv], static_cast<const T*>(a.z) + row * a.zs + ev);
-        }
-        cp_commit();
-    };
-    float bq[NBC], cq[NBC];
-    auto fetch_bc = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < NBC; ++i) {
-            const int k = tid + i * kThreads, row = k / NP, n = k % NP;
-            const bool ok = k < TT * NP && t + row < p.t1 && n < a.N;
-            bq[i] = ok ? ld_f(Bp + (int64_t)(t + row) * a.bcs + n) : 0.0f;
-            cq[i] = ok ? ld_f(Cp + (int64_t)(t + row) * a.bcs + n) : 0.0f;
+        for (int j = 0; j < 2; ++j) {
+            kept[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (live[j]) kept[j] = __ldcs(reinterpret_cast<const float4*>(ws.ckpt + (ck0 + g) * st_all + st[j]));
         }
     };
-    auto raw8 = [&](int buf, int i) { return smem_row8(&sm.raw[buf][i][sr][8 * sv]); };
-
-    const int ntile = (p.t1 - p.t0 + TT - 1) / TT;
-    const int64_t ck0 = (int64_t)p.r * ckpts_of(a.L) + (p.t0 - p.s0) / kDiagCkpt;   // the piece's first kept state
-    fetch(p.t0 + (ntile - 1) * TT, 0);
-    fetch_bc(p.t0 + (ntile - 1) * TT);
-    int buf = 0;
-    for (int it = ntile - 1; it >= 0; --it, buf ^= 1) {
-        const int t = p.t0 + it * TT;
-        cp_wait_all();   // a thread reads back what it copied itself
-        if (tid < TL::NVEC) {
-            const bool ok = loads && t + sr < p.t1;
-            const Raw8<T> u = raw8(buf, 0), v = raw8(buf, 1), dy = raw8(buf, 2), z = raw8(buf, 3);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (ok) {
-                    f.x = softplus_series(v.get(j) + bias[j]);
-                    f.y = f.x * u.get(j);
-                    f.z = dy.get(j);
-                    if (gated) f.z *= z.get(j) * sigmoid_f(z.get(j));
-                }
-                sm.tile[sr][TL::col16(8 * sv + j, 0)] = f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NBC; ++i) {
-            const int k = tid + i * kThreads;
-            if (k < TT * NP) {
-                reinterpret_cast<float*>(sm.B)[k] = bq[i];
-                reinterpret_cast<float*>(sm.C)[k] = cq[i];
-            }
+    static_assert(kDiagCkpt == 4, "the walk takes a group of 4 rows from a kept state");
+    fetch_kept((p.t1 - p.t0 - 1) / 4);
+    for (int w = 0; w < ntile; ++w) {
+        const int buf = w & 1, t = tile_row(w);
+        if (lower) {
+            lay_out(w);
+            if (w > 0) sum_warps(w - 1);
+        } else {
+            lay_out_bc();
+            if (w > 0) finish(w - 1);
         }
         __syncthreads();
-        if (it > 0) {
-            fetch(t - TT, buf ^ 1);
-            fetch_bc(t - TT);
-        }
-
+        if (lower) fetch(w + 1);
+        else fetch_bc(w + 1);
 #pragma unroll 1
-        for (int half = TT / kDiagCkpt - 1; half >= 0; --half) {
-            const int r0 = half * kDiagCkpt;
-            if (t + r0 >= p.t1) continue;
-            // forward over 8 rows: decays and states
-            float2 av[kDiagCkpt][2][2], hv[kDiagCkpt + 1][2][2];
-            const float* ck = ws.ckpt + (ck0 + (it * TT + r0) / kDiagCkpt) * st_all;
+        for (int gr = (min(TT, p.t1 - t) - 1) / 4; gr >= 0; --gr) {
+            float h[2][4];
+            put4(kept[0], h[0]);
+            put4(kept[1], h[1]);
+            const int before = (t - p.t0) / 4 + gr - 1;
+            if (before >= 0) fetch_kept(before);
+            // forward over the 4 rows
+            float2 av[2][2][4], qv[2][2][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (live[j]) v = __ldcs(reinterpret_cast<const float4*>(ck + st[j]));
-                hv[0][j][0] = make_float2(v.x, v.y);
-                hv[0][j][1] = make_float2(v.z, v.w);
-            }
-#pragma unroll
-            for (int i = 0; i < kDiagCkpt; ++i) {
-                const float4 b4 = sm.B[r0 + i][q];
+            for (int i = 0; i < 2; ++i) {
+                const int pr = 2 * gr + i;
+                const float4 bb[2] = {sm.B[pr][0][m][q], sm.B[pr][1][m][q]}, cc[2] = {sm.C[pr][0][m][q], sm.C[pr][1][m][q]};
+                float2 sC[4], ys[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float2 d = *reinterpret_cast<const float2*>(&sm.tile[r0 + i][col[j]]);
-                    const float2 dd = make_float2(d.x, d.x), xx = make_float2(d.y, d.y);
-                    const float2 s0 = pk_mul(A2[j][0], dd), s1 = pk_mul(A2[j][1], dd);
-                    av[i][j][0] = make_float2(ex2(s0.x), ex2(s0.y));
-                    av[i][j][1] = make_float2(ex2(s1.x), ex2(s1.y));
-                    hv[i + 1][j][0] = pk_fma(av[i][j][0], hv[i][j][0], pk_mul(make_float2(b4.x, b4.y), xx));
-                    hv[i + 1][j][1] = pk_fma(av[i][j][1], hv[i][j][1], pk_mul(make_float2(b4.z, b4.w), xx));
+                    const float4 d = sm.tile[buf][pr][TL::col16(cl[j], pr)];
+                    const float2 pp = sm.p[buf][pr][TL::col8(cl[j], pr)];
+                    const float2 dd = make_float2(d.x, d.y), xx = make_float2(d.z, d.w);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 b2 = k & 1 ? make_float2(bb[k >> 1].z, bb[k >> 1].w) : make_float2(bb[k >> 1].x, bb[k >> 1].y);
+                        const float2 c2 = k & 1 ? make_float2(cc[k >> 1].z, cc[k >> 1].w) : make_float2(cc[k >> 1].x, cc[k >> 1].y);
+                        av[i][j][k] = make_float2(ex2(A2[j][k] * dd.x), ex2(A2[j][k] * dd.y));
+                        const float2 xb = pk_mul(xx, b2);
+                        const float q0 = av[i][j][k].x * h[j][k], h0 = q0 + xb.x;
+                        const float q1 = av[i][j][k].y * h0, h1 = q1 + xb.y;
+                        qv[i][j][k] = make_float2(q0, q1);
+                        h[j][k] = h1;
+                        const float2 hh = make_float2(h0, h1);
+                        sC[k] = j ? pk_fma(hh, pp, sC[k]) : pk_mul(hh, pp);
+                        if (gated) ys[j] = k ? pk_fma(hh, c2, ys[j]) : pk_mul(hh, c2);
+                    }
+                }
+                channel_sum<LPC>(sC, cg, [&](int row, int slot, float v) { red[warp][2 * pr + row][n0 + (slot ^ m)].y = v; });
+                if (gated) {
+                    // over a channel's lanes: slot 0's channel is kept (diag_tile.cuh), then a row
+                    const float2 y = ex(ys[0], ys[1], LPC / 2);
+                    if constexpr (LPC >= 4) {
+                        const int odd = q & 1;
+                        float v = ex(odd ? y.y : y.x, odd ? y.x : y.y, 1);
+#pragma unroll
+                        for (int o = 2; o < LPC / 2; o <<= 1) v = ex(v, v, o);
+                        y_sum[2 * pr + odd][cl[0]] = v;
+                    } else {
+                        y_sum[2 * pr][cl[0]] = y.x;
+                        y_sum[2 * pr + 1][cl[0]] = y.y;
+                    }
                 }
             }
             // and back
 #pragma unroll
-            for (int i = kDiagCkpt - 1; i >= 0; --i) {
-                const int row = r0 + i;
-                const float4 b4 = sm.B[row][q], c4 = sm.C[row][q];
-                const float2 b01 = make_float2(b4.x, b4.y), b23 = make_float2(b4.z, b4.w);
-                const float2 c01 = make_float2(c4.x, c4.y), c23 = make_float2(c4.z, c4.w);
-                float sn[4], sy[2];       // state sums: gB, w A of each channel; y
-                float2 sB[2], sC[2];      // channel sums
+            for (int i = 1; i >= 0; --i) {
+                const int pr = 2 * gr + i;
+                const float4 bb[2] = {sm.B[pr][0][m][q], sm.B[pr][1][m][q]}, cc[2] = {sm.C[pr][0][m][q], sm.C[pr][1][m][q]};
+                float2 sB[4], gb[2], wa[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float4 d = sm.tile[row][col[j]];
-                    const float2 pp = make_float2(d.z, d.z), xx = make_float2(d.y, d.y), dd = make_float2(d.x, d.x);
-                    const float2 g0 = pk_fma(c01, pp, G[j][0]), g1 = pk_fma(c23, pp, G[j][1]);
-                    const float2 gb = pk_fma(g0, b01, pk_mul(g1, b23));
-                    sn[2 * j] = gb.x + gb.y;
-                    if (j == 0) {
-                        sB[0] = pk_mul(g0, xx); sB[1] = pk_mul(g1, xx);
-                        sC[0] = pk_mul(hv[i + 1][j][0], pp); sC[1] = pk_mul(hv[i + 1][j][1], pp);
-                    } else {
-                        sB[0] = pk_fma(g0, xx, sB[0]); sB[1] = pk_fma(g1, xx, sB[1]);
-                        sC[0] = pk_fma(hv[i + 1][j][0], pp, sC[0]); sC[1] = pk_fma(hv[i + 1][j][1], pp, sC[1]);
-                    }
-                    G[j][0] = pk_mul(av[i][j][0], g0);
-                    G[j][1] = pk_mul(av[i][j][1], g1);
-                    const float2 w0 = pk_mul(G[j][0], hv[i][j][0]), w1 = pk_mul(G[j][1], hv[i][j][1]);
-                    dA[j][0] = pk_fma(w0, dd, dA[j][0]);
-                    dA[j][1] = pk_fma(w1, dd, dA[j][1]);
-                    const float2 wa = pk_fma(w0, A2[j][0], pk_mul(w1, A2[j][1]));
-                    sn[2 * j + 1] = wa.x + wa.y;
-                    if (gated) {
-                        const float2 yy = pk_fma(hv[i + 1][j][0], c01, pk_mul(hv[i + 1][j][1], c23));
-                        sy[j] = yy.x + yy.y;
+                    const float4 d = sm.tile[buf][pr][TL::col16(cl[j], pr)];
+                    const float2 pp = sm.p[buf][pr][TL::col8(cl[j], pr)];
+                    const float2 dd = make_float2(d.x, d.y), xx = make_float2(d.z, d.w);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 b2 = k & 1 ? make_float2(bb[k >> 1].z, bb[k >> 1].w) : make_float2(bb[k >> 1].x, bb[k >> 1].y);
+                        const float2 c2 = k & 1 ? make_float2(cc[k >> 1].z, cc[k >> 1].w) : make_float2(cc[k >> 1].x, cc[k >> 1].y);
+                        const float g1 = fmaf(c2.y, pp.y, G[j][k]);
+                        const float g0 = fmaf(c2.x, pp.x, av[i][j][k].y * g1);
+                        G[j][k] = av[i][j][k].x * g0;
+                        const float2 gg = make_float2(g0, g1);
+                        gb[j] = k ? pk_fma(gg, b2, gb[j]) : pk_mul(gg, b2);
+                        sB[k] = j ? pk_fma(gg, xx, sB[k]) : pk_mul(gg, xx);
+                        const float2 w2 = pk_mul(gg, qv[i][j][k]);
+                        dA[j][k] = pk_fma(w2, dd, dA[j][k]);
+                        // (scalar: a pair of A would have to be copied together)
+                        wa[j] = k ? make_float2(fmaf(w2.x, A2[j][k], wa[j].x), fmaf(w2.y, A2[j][k], wa[j].y))
+                                  : make_float2(w2.x * A2[j][k], w2.y * A2[j][k]);
                     }
                 }
-                float sc[8] = {sB[0].x, sB[0].y, sB[1].x, sB[1].y, sC[0].x, sC[0].y, sC[1].x, sC[1].y};
-                int at = 0;
-                scatter_sum<8, NL, LPC>(sc, cg, at);
+                channel_sum<LPC>(sB, cg, [&](int row, int slot, float v) { red[warp][2 * pr + row][n0 + (slot ^ m)].x = v; });
+                const float2 vg = ex(gb[0], gb[1], LPC / 2), vw = ex(wa[0], wa[1], LPC / 2);
+                if constexpr (LPC >= 4) {
+                    const bool odd = q & 1;
+                    float2 v = ex(odd ? vw : vg, odd ? vg : vw, 1);
 #pragma unroll
-                for (int k = 0; k < (NL < 8 ? 8 / NL : 1); ++k)
-                    reinterpret_cast<float*>(&sm.red[warp][row][n0 + ((at + k) & 3)])[(at + k) >> 2] = sc[k];
-                // every lane keeps the channel of its slot 0 (diag_tile.cuh)
-                float v[2] = {sn[0] + __shfl_xor_sync(0xffffffffu, sn[2], LPC / 2), sn[1] + __shfl_xor_sync(0xffffffffu, sn[3], LPC / 2)};
-                at = 0;
-                scatter_sum<2, LPC / 2, 1>(v, q % (LPC / 2), at);
-#pragma unroll
-                for (int k = 0; k < (LPC == 2 ? 2 : 1); ++k) reinterpret_cast<float*>(&sm.tile[row][col[0]])[2 * (at + k) + 1] = v[k];
-                if (gated) {
-                    float y = sy[0] + __shfl_xor_sync(0xffffffffu, sy[1], LPC / 2);
-#pragma unroll
-                    for (int o = LPC / 4; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                    sm.ysum[row][col[0]] = y;
+                    for (int o = 2; o < LPC / 2; o <<= 1) v = ex(v, v, o);
+                    float(*to)[CH] = odd ? wa_sum : gb_sum;
+                    to[2 * pr][cl[0]] = v.x;
+                    to[2 * pr + 1][cl[0]] = v.y;
+                } else {
+                    gb_sum[2 * pr][cl[0]] = vg.x;
+                    gb_sum[2 * pr + 1][cl[0]] = vg.y;
+                    wa_sum[2 * pr][cl[0]] = vw.x;
+                    wa_sum[2 * pr + 1][cl[0]] = vw.y;
                 }
             }
         }
         __syncthreads();
-        // the loading threads finish their 8 channels of a row
-        if (loads && t + sr < p.t1) {
-            const Raw8<T> u = raw8(buf, 0), v = raw8(buf, 1), dy = raw8(buf, 2), z = raw8(buf, 3);
-            float du[8], ddt[8], dz[8];
+    }
+    if (lower) sum_warps(ntile - 1);
+    else finish(ntile - 1);
+    __syncthreads();
+    for (int c = tid; c < e_end - e0; c += kThreads) {
+        float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = TL::col16(8 * sv + j, 0);
-                const float4 f = sm.tile[sr][c];
-                const float uv = u.get(j);
-                du[j] = fmaf(Dv[j], f.z, f.x * f.y);
-                ddt[j] = fmaf(uv, f.y, f.w * kLn2) * sigmoid_f(v.get(j) + bias[j]);
-                dDs[j] = fmaf(uv, f.z, dDs[j]);
-                dbs[j] += ddt[j];
-                if (gated) {
-                    const float zv = z.get(j);
-                    dz[j] = dy.get(j) * fmaf(Dv[j], uv, sm.ysum[sr][c]) * dsilu_f(zv, sigmoid_f(zv));
-                }
-            }
-            const int64_t o = (int64_t)(t + sr) * a.E + ev;
-            Raw8<T>::store(static_cast<T*>(ba.du) + o, du);
-            Raw8<T>::store(static_cast<T*>(ba.ddt) + o, ddt);
-            if (gated) Raw8<T>::store(static_cast<T*>(ba.dz) + o, dz);
+        for (int r = 0; r < PAIRS; ++r) {
+            const float2 v = tails[c & 7][r * VPR + (c >> 3)];
+            s.x += v.x;
+            s.y += v.y;
         }
-        const int rows = min(TT, p.t1 - t);
-        for (int k = tid; k < rows * NP; k += kThreads) {
-            const int row = k / NP, n = k % NP;
-            if (n < a.N) {
-                float2 s = sm.red[0][row][n];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) {
-                    s.x += sm.red[w][row][n].x;
-                    s.y += sm.red[w][row][n].y;
-                }
-                reinterpret_cast<float2*>(ws.bc)[((int64_t)blockIdx.y * a.rows + t + row) * a.N + n] = s;
-            }
-        }
+        ws.dD[p.idx * a.E + e0 + c] = s.x;
+        ws.dbias[p.idx * a.E + e0 + c] = s.y;
     }
 
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (!live[j]) continue;
         if (p.t0 == p.s0 && ba.dinit)
-            *reinterpret_cast<float4*>(ba.dinit + p.r * st_all + st[j]) = make_float4(G[j][0].x, G[j][0].y, G[j][1].x, G[j][1].y);
-        *reinterpret_cast<float4*>(ws.dA + p.idx * st_all + st[j]) = make_float4(dA[j][0].x, dA[j][0].y, dA[j][1].x, dA[j][1].y);
-    }
-    // dD, ddt_bias: over the tile's rows through shared memory
-    __syncthreads();
-    if (loads)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) *reinterpret_cast<float2*>(&sm.tile[sr][8 * sv + j]) = make_float2(dDs[j], dbs[j]);
-    __syncthreads();
-    for (int c = tid; c < e_end - e0; c += kThreads) {
-        float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int r = 0; r < TT; ++r) {
-            const float2 v = *reinterpret_cast<const float2*>(&sm.tile[r][c]);
-            s.x += v.x;
-            s.y += v.y;
-        }
-        ws.dD[p.idx * a.E + e0 + c] = s.x;
-        ws.dbias[p.idx * a.E + e0 + c] = s.y;
+            *reinterpret_cast<float4*>(ba.dinit + p.r * st_all + st[j]) = order4(make_float4(G[j][0], G[j][1], G[j][2], G[j][3]), m);
+        *reinterpret_cast<float4*>(ws.dA + p.idx * st_all + st[j]) =
+            order4(make_float4(dA[j][0].x + dA[j][0].y, dA[j][1].x + dA[j][1].y, dA[j][2].x + dA[j][2].y, dA[j][3].x + dA[j][3].y), m);
     }
 }
 
@@ -376,18 +525,19 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
     }
 }
 
-// Rows per piece.  The kernel's time is that of its fullest SM, so the rows
-// are cut until the CTAs make kWaves of what the device holds at a time: a
-// last, partly filled wave then costs little.
-constexpr int kCtasAtATime = 148 * 2;
-constexpr int kWaves = 6;
+// Rows per piece.  The forward walk pays for the pieces (306 us without, 610
+// with them, at 8 x 2048 rows of 2560 channels), so rows are cut only where
+// whole sequences leave SMs with less than kLeastPerSm CTAs, and then until
+// there are kCutPerSm.
+constexpr int kLeastPerSm = 12;
+constexpr int kCutPerSm = 15;
 constexpr int kPieceLeast = 64;
 
 int bwd_piece_rows(int b, int L, int E, int N, int G)
 {
     const int64_t ctas = (int64_t)b * channel_tiles(E, G, kWarps * 64 / tile_lanes(N)) * G;
-    const int64_t pieces = (kCtasAtATime * kWaves + ctas - 1) / ctas;
-    if (pieces < 2) return L;
+    if (ctas >= (int64_t)sm_count() * kLeastPerSm) return L;
+    const int64_t pieces = ((int64_t)sm_count() * kCutPerSm + ctas - 1) / ctas;
     int64_t seg = ((int64_t)L + pieces - 1) / pieces;
     seg = (seg + 31) / 32 * 32;
     if (seg < kPieceLeast) seg = kPieceLeast;
@@ -425,17 +575,21 @@ template <typename T, int LPC>
 cudaError_t launch_lpc(const DiagBwdArgs& a, const Plan& p, const BwdWs& ws, cudaStream_t s)
 {
     const int smem = (int)sizeof(Smem<T, LPC>);
-    if (smem > 48 * 1024) {
+    if (smem > 16 * 1024) {   // with the kernel's own arrays, beyond what needs no leave
         const cudaError_t e = cudaFuncSetAttribute((const void*)diag_bwd_kernel<T, LPC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    diag_bwd_kernel<T, LPC><<<dim3((unsigned)p.pieces, (unsigned)(p.tiles * a.f.G)), kThreads, smem, s>>>(a, ws, p.seg);
+    const int64_t grid = p.pieces * p.tiles * a.f.G;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    diag_bwd_kernel<T, LPC><<<(unsigned)grid, kThreads, smem, s>>>(a, ws, p.seg);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_t(const DiagBwdArgs& a, const Plan& p, const BwdWs& ws, cudaStream_t s)
+cudaError_t launch_t(const DiagBwdArgs& args, const Plan& p, const BwdWs& ws, cudaStream_t s)
 {
+    DiagBwdArgs a = args;
+    a.f.bc_aligned = bc_aligned(a.f, sizeof(T));
     cudaError_t e;
     switch (tile_lanes(a.f.N)) {
         case 2: e = launch_lpc<T, 2>(a, p, ws, s); break;

@@ -34,7 +34,7 @@ template <int LPC, int WARPS> struct DiagTile {
     {
         const int q = lane % LPC, cg = lane / LPC;
         const int swap = LPC > 1 ? (q / (LPC / 2)) & 1 : 0;
-        return warp * 2 * NL + (j ^ swap) * NL + cg;
+        return warp * 2 * NL + 2 * cg + (j ^ swap);   // neighbours: 8 lanes read 4 adjacent entries
     }
     // Where channel c lies in a line of 16-byte (8-byte: col8) entries.  A
     // loading thread writes 8 adjacent channels; their order is turned by the
