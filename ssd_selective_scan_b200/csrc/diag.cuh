@@ -279,6 +279,8 @@ __device__ inline bool find_piece_packed(int q, const Slots& sl, int rows, int s
     if (second - p.s0 <= keep) second += seg;           // (keep < seg)
     const int64_t cut = p.t0 == p.s0 ? second : (int64_t)p.t0 + seg;
     p.t1 = (int)(cut < p.s1 ? cut : p.s1);
+    // the piece behind this one is found by its row's request: is it this one?
+    if (cut < p.s1 && sl.seq_of[cut] != p.r) flag_invalid(sl.status);
     p.idx = q;
     p.first = p.r;
     p.next = sl.nseq + second / seg - 1;

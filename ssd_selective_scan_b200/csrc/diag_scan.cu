@@ -363,9 +363,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) diag_scan_ke
     const int keep_end = min(p.t1, p.s1 - 1);   // the sequence's last state is written behind the walk
     float sdt[2] = {0.0f, 0.0f};
     // the backward pieces' part: P the product of the decays since the
-    // piece's start, Gl = sum_t P_t C_t p_t (of even and odd rows)
-    float P[2][4];
-    float2 Gl[2][4];
+    // piece's start, Gl = sum_t P_t C_t p_t
+    float P[2][4], Gl[2][4];
     auto restart = [&] {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) diag_scan_ke
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 P[j][n] = 1.0f;
-                Gl[j][n] = make_float2(0.0f, 0.0f);
+                Gl[j][n] = 0.0f;
             }
         }
     };
@@ -426,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) diag_scan_ke
                             } else {
                                 const float P0 = P[j][n] * a0;
                                 P[j][n] = P0 * a1;
-                                Gl[j][n] = pk_fma(make_float2(P0, P[j][n]), pk_mul(c2, pp), Gl[j][n]);
+                                const float2 cp = pk_mul(c2, pp);
+                                Gl[j][n] = fmaf(P[j][n], cp.y, fmaf(P0, cp.x, Gl[j][n]));
                             }
                         }
                     }
@@ -481,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) diag_scan_ke
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         if (live[j]) {
-                            const float g[4] = {Gl[j][0].x + Gl[j][0].y, Gl[j][1].x + Gl[j][1].y, Gl[j][2].x + Gl[j][2].y, Gl[j][3].x + Gl[j][3].y};
-                            put4(a.gl + i * st_all + st[j], g);
+                            put4(a.gl + i * st_all + st[j], Gl[j]);
                             if (q == 0) a.gsdt[i * a.E + e0 + cl[j]] = sdt[j];
                         }
                     restart();

@@ -484,51 +484,67 @@ __global__ void __launch_bounds__(kThreads, 3) diag_bwd_kernel(const DiagBwdArgs
     }
 }
 
-// dB, dC: the sum over a group's channel tiles of part [G][tiles][rows][N].
-template <typename T>
-__global__ void __launch_bounds__(256) sum_bc_kernel(const float2* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC, int tiles,
-                                                     int64_t rows, int N, int G)
-{
-    const int64_t per = rows * N;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int g = blockIdx.y;
-    if (i >= per) return;
-    const float2* src = part + (int64_t)g * tiles * per + i;
-    float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-    for (int k = 0; k < tiles; ++k) {
-        const float2 v = __ldcs(src + k * per);
-        s.x += v.x;
-        s.y += v.y;
-    }
-    const int64_t row = i / N, o = (row * G + g) * N + (i - row * N);
-    dB[o] = io<T>::from_f(s.x);
-    dC[o] = io<T>::from_f(s.y);
-}
+// The partial sums, in a fixed order, one launch for all.  The first bc_blocks
+// CTAs: dB and dC, over a group's channel tiles of bc [G][tiles][rows][N].  The
+// others: 32 columns each of dA, then dD, then ddt_bias [pieces][cols], 8 lanes
+// of pieces joined in shared memory.
+struct SumArgs {
+    const float2* bc;
+    const float* part[3];
+    float* out[3];
+    int64_t cols[3];
+    void *dB, *dC;
+    int64_t rows, pieces, bc_blocks;
+    int tiles, N, G;
+};
+constexpr int kSumThreads = 256;
 
-// Columns of part [parts][cols], 32 x 8 threads: 8 lanes of parts, joined in
-// a fixed order.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, float* __restrict__ out, int64_t parts, int64_t cols)
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads) diag_sum_kernel(const SumArgs a)
 {
     __shared__ float sums[8][32];
-    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    if (blockIdx.x < a.bc_blocks) {
+        const int64_t per = a.rows * a.N;
+        const int64_t at = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
+        if (at >= per * a.G) return;
+        const int64_t g = at / per, i = at - g * per;
+        const float2* src = a.bc + g * a.tiles * per + i;
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = 0; k < a.tiles; ++k) {
+            const float2 v = __ldcs(src + k * per);
+            s.x += v.x;
+            s.y += v.y;
+        }
+        const int64_t row = i / a.N, o = (row * a.G + g) * a.N + (i - row * a.N);
+        static_cast<T*>(a.dB)[o] = io<T>::from_f(s.x);
+        static_cast<T*>(a.dC)[o] = io<T>::from_f(s.y);
+        return;
+    }
+    int64_t block = blockIdx.x - a.bc_blocks;
+    int which = 0;
+    while (block >= (a.cols[which] + 31) / 32) block -= (a.cols[which++] + 31) / 32;
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+    const int64_t cols = a.cols[which], col = block * 32 + x;
     float s = 0.0f;
     if (col < cols)
-        for (int64_t i = threadIdx.y; i < parts; i += 8) s += part[i * cols + col];
-    sums[threadIdx.y][threadIdx.x] = s;
+        for (int64_t i = y; i < a.pieces; i += 8) s += a.part[which][i * cols + col];
+    sums[y][x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && col < cols) {
+    if (y == 0 && col < cols) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
-        out[col] = s;
+        for (int i = 0; i < 8; ++i) s += sums[i][x];
+        a.out[which][col] = s;
     }
 }
 
-// Rows per piece.  The forward walk pays for the pieces (306 us without, 610
-// with them, at 8 x 2048 rows of 2560 channels), so rows are cut only where
-// whole sequences leave SMs with less than kLeastPerSm CTAs, and then until
-// there are kCutPerSm.
+// Rows per piece.  The forward walk pays for the pieces (306 us without, 468
+// with them, at 8 x 2048 rows of 2560 channels), this kernel gains from them
+// (1390 us whole, 2 or 3 CTAs on an SM for all of its time; 990 cut), so rows
+// are cut where whole sequences make less than kLeastPerSm CTAs an SM, which
+// holds 3 at a time, and then until there are kCutPerSm (9 and 24 are within
+// 1.5%).
 constexpr int kLeastPerSm = 12;
 constexpr int kCutPerSm = 15;
 constexpr int kPieceLeast = 64;
@@ -598,9 +614,13 @@ cudaError_t launch_t(const DiagBwdArgs& args, const Plan& p, const BwdWs& ws, cu
         default: e = launch_lpc<T, 16>(a, p, ws, s); break;
     }
     if (e != cudaSuccess) return e;
-    const int64_t per = (int64_t)a.f.rows * a.f.N;
-    sum_bc_kernel<T><<<dim3((unsigned)((per + 255) / 256), (unsigned)a.f.G), 256, 0, s>>>(
-        reinterpret_cast<const float2*>(ws.bc), static_cast<T*>(a.dB), static_cast<T*>(a.dC), p.tiles, a.f.rows, a.f.N, a.f.G);
+    const int64_t E = a.f.E, items = (int64_t)a.f.rows * a.f.N * a.f.G;
+    SumArgs sum{reinterpret_cast<const float2*>(ws.bc), {ws.dA, ws.dD, ws.dbias}, {a.dA, a.dD, a.ddt_bias}, {E * a.f.N, E, E}, a.dB, a.dC,
+                a.f.rows, p.pieces, (items + kSumThreads - 1) / kSumThreads, p.tiles, a.f.N, a.f.G};
+    int64_t grid = sum.bc_blocks;
+    for (const int64_t c : sum.cols) grid += (c + 31) / 32;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    diag_sum_kernel<T><<<(unsigned)grid, kSumThreads, 0, s>>>(sum);
     return cudaGetLastError();
 }
 
@@ -623,14 +643,6 @@ cudaError_t launch_diag_scan_bwd(const DiagBwdArgs& a, cudaStream_t s)
     f.bseg = p.seg;
     cudaError_t e = launch_diag_ckpt(f, s);
     if (e == cudaSuccess) e = a.f.bf16 ? launch_t<__nv_bfloat16>(a, p, ws, s) : launch_t<float>(a, p, ws, s);
-    auto sum = [&](const float* part, float* out, int64_t cols) {
-        if (e != cudaSuccess) return;
-        sum_parts_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, 8), 0, s>>>(part, out, p.pieces, cols);
-        e = cudaGetLastError();
-    };
-    sum(ws.dA, a.dA, (int64_t)a.f.E * a.f.N);
-    sum(ws.dD, a.dD, a.f.E);
-    sum(ws.dbias, a.ddt_bias, a.f.E);
     return e;
 }
 

@@ -11,6 +11,9 @@
 // of a channel do not each load and compute them again.  A, D and dt_bias are
 // read once for the rows.  y's sums over a channel's lanes are exchanged for
 // all rows at once, each lane ending with some of the rows.
+//
+// 256 rows of 8192 bf16 channels, 16 states: 56 us, 5.1 TB/s, 77% of the
+// measured copy rate (8 rows a CTA, 7 CTAs an SM: 60 us; 16 rows: 73).
 #include "diag.cuh"
 #include "diag.h"
 
@@ -18,10 +21,11 @@ namespace ssd {
 namespace {
 
 constexpr int kUpdThreads = 128;
-constexpr int kUpdRows = 8;
+constexpr int kUpdRows = 4;
+constexpr int kUpdCtas = 12;   // per SM
 
 template <typename T, int LPC, int ROWS>
-__global__ void __launch_bounds__(kUpdThreads) diag_update_kernel(const DiagArgs a)
+__global__ void __launch_bounds__(kUpdThreads, kUpdCtas) diag_update_kernel(const DiagArgs a)
 {
     constexpr int CH = kUpdThreads / LPC, NP = 4 * LPC;
     __shared__ float2 dx[ROWS][CH];                   // dt, x = dt u; y takes dt's place

@@ -516,6 +516,7 @@ def _spoilt():
     yield "slot negative", put("slot_of", 39, -2), False
     yield "request out of range", put("seq_of", 32, 99), True
     yield "request of other rows", put("seq_of", 32, 2), True
+    yield "no request for a row", put("seq_of", 32, -1), True
 
 
 @pytest.mark.parametrize("what,spoil,by_row", list(_spoilt()), ids=[w[0].replace(" ", "_") for w in _spoilt()])
@@ -536,6 +537,17 @@ def test_unsound_maps_are_reported(what, spoil, by_row):
     assert st.item() == 1, what
     for pool in (states, cache):
         assert (pool[0] == 0).all() and (pool[-1] == 0).all()
+
+
+def test_cut_scan_reports_rows_without_their_request():
+    """Pieces of a cut sequence are found by their first row's request."""
+    q = R.batch([900], [0], 64)
+    m = R.ref_map(q, 900)
+    m["seq_of"][256:] = [-1] * 644
+    p = R.scan_inputs((900,), 16, 16, 1, F32, seed=1, device="cuda")
+    states, st = torch.zeros(q["nslots"], 16, 16, device="cuda"), zero_status()
+    ssd.diag_scan_fwd_varlen(**p, states=states, m=dev_map(m, 64), status=st)
+    assert st.item() == 1
 
 
 def test_state_update_refuses_two_rows_of_a_request():
