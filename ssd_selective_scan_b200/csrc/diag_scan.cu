@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) diag_scan_ke
             }
         };
         if (groups == TT / 4 && !(PACKED && OUT && keep < t + TT)) {
-#pragma unroll
+#pragma unroll 2
             for (int gr = 0; gr < TT / 4; ++gr) walk4(gr, std::false_type{});
         } else {
 #pragma unroll 1
