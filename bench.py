@@ -397,6 +397,35 @@ class DecodeStep:
                                s.H, s.P, s.G, s.N, dt_bias=d["dt_bias"], D=d["D"], y=self.y)
 
 
+class DiagStep:
+    """The diagonal scan's calls on the 3B layer's rows and inner width (the
+    8B layer's for the single-token update), 16 states per channel."""
+    SHAPES = {"diag": (8, 2048, 2560), "diag_bwd": (8, 2048, 2560), "diag_step": (256, 1, 8192)}
+    N = 16
+
+    def __init__(self, which, seq_len, seed, dev):
+        import ssd_selective_scan_b200 as ssd
+        self.ssd, self.which = ssd, which
+        b, L, E = self.SHAPES[which]
+        L = L if seq_len is None else seq_len
+        self.name = f"{which}_b{b}_L{L}_e{E}_n{self.N}"
+        d = {k: v.to(dev) for k, v in synth.diag_inputs(b, L, E, self.N, seed).items()}
+        if which == "diag_step":
+            d |= {k: d[k][:, 0].contiguous() for k in ("u", "dt_raw", "z", "B", "C")}
+            self.states = torch.zeros(b, E, self.N, device=dev)
+        if which == "diag_bwd":
+            self.dy = torch.randn(b, L, E, device=dev).to(torch.bfloat16)
+        self.d = d
+
+    def __call__(self):
+        if self.which == "diag":
+            self.ssd.diag_scan_fwd(**self.d)
+        elif self.which == "diag_bwd":
+            self.ssd.diag_scan_bwd(**self.d, dy=self.dy)
+        else:
+            self.ssd.diag_state_update(self.states, **self.d)
+
+
 def _events(n):
     return [torch.cuda.Event(enable_timing=True) for _ in range(n)]
 
@@ -810,6 +839,8 @@ def run_one_kernel(args, dev):
         fn = BackwardStep(s, synth.config_seed(1), dev)
     elif args.kernel == "ragged":
         fn = RaggedStep(RAGGED, synth.config_seed(1), dev)
+    elif args.kernel in DiagStep.SHAPES:
+        fn = DiagStep(args.kernel, args.seq_len, synth.config_seed(1), dev)
     else:
         s = synth.CONFIGS[args.workload]
         if args.seq_len is not None:
@@ -827,7 +858,7 @@ def run_one_kernel(args, dev):
     e1.record()
     torch.cuda.synchronize()
     workload = {"decode": DECODE.name, "mixer": MIXER.name, "linear": MIXER.name, "bwd": BWD.name,
-                "ragged": RAGGED.name + " as a prompt-length mix"}.get(args.kernel, args.workload)
+                "ragged": RAGGED.name + " as a prompt-length mix"}.get(args.kernel, getattr(fn, "name", args.workload))
     print(json.dumps({"kernel": args.kernel, "workload": workload, "seq_len": args.seq_len,
                       "launches": args.steps, "ms_per_launch": e0.elapsed_time(e1) / args.steps}), flush=True)
 
@@ -839,7 +870,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--impl", choices=["ours", "reference"], default="ours")
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--kernel", choices=["scan", "conv", "decode", "bwd", "mixer", "linear", "ragged"],
+    ap.add_argument("--kernel", choices=["scan", "conv", "decode", "bwd", "mixer", "linear", "ragged", *DiagStep.SHAPES],
                     help="launch only this kernel (warmup + steps launches) and print its mean "
                          "CUDA-event time; for profiler captures")
     ap.add_argument("--workload", type=int, choices=PREFILL_CONFIGS, default=HEADLINE,

@@ -8,7 +8,9 @@
 // matrix product to hand to the tensor cores: the work is one exponential and
 // four FMAs per (token, channel, state).  What bounds it is the
 // special-function unit (16 results per cycle and SM: N = 16 states cost a
-// cycle per token and channel), before HBM (8 bytes per token and channel).
+// cycle per token and channel) and instruction issue, before HBM (8 bytes per
+// token and channel).  8 x 2048 tokens of 2560 gated bf16 channels: 347 us,
+// both at about 60% while an SM has work; 144 us for the exponentials alone.
 //
 // Layout.  A CTA covers CH channels of one group (diag_tile.cuh) and walks
 // the tokens of a piece of a sequence in tiles of TT.  Two warps hold the

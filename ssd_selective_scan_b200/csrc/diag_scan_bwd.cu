@@ -37,12 +37,15 @@
 //
 // The walk is four fifths of the work here, so all four warps walk (half of
 // them feeding the others, as in the forward scan, took 1700 us where this
-// takes the time below).  Between two tiles' walks one half of the CTA lays
+// takes 990).  Between two tiles' walks one half of the CTA lays
 // out the next tile (u, dt_raw, dy and z by cp.async a tile ahead; dt, x and p
 // formed once per token and channel) while the other finishes du, ddt_raw and
 // dz of the last one from its sums, in 16-byte vectors.
 //
-// Bound by instruction issue, not by HBM.
+// 8 x 2048 tokens of 2560 gated bf16 channels, 16 states: 990 us, the forward
+// walk 468, the sums 15.  Bound by instruction issue (27 per token, channel
+// and state, 53% of the issue slots: 168 registers hold the 4 rows, so 12
+// warps share an SM) and by shared memory's wavefronts (54%), not by HBM.
 #include "diag_tile.cuh"
 
 namespace ssd {

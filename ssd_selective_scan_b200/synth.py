@@ -212,3 +212,15 @@ def ragged_lengths(total: int, seed: int, lo: int = 64, hi: int = 4096) -> list:
         lens.append(n)
         left -= n
     return lens
+
+
+def diag_inputs(b: int, L: int, E: int, N: int, seed: int, *, G: int = 1, dtype: torch.dtype = torch.bfloat16) -> dict:
+    """Inputs of the diagonal scan, host tensors: u, z [b, L, E] ~ N(0, 1), dt_raw
+    [b, L, E] ~ U(-4, -1), B, C [b, L, G, N] ~ N(0, 1)/sqrt(N) (I/O dtype), A
+    [E, N] = -(1 .. N) times exp(N(0, 0.09)) per element, dt_bias [E] = 0, D [E]
+    ~ N(1, 0.09) (float32)."""
+    g = _gen(seed)
+    rn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    return dict(u=rn(b, L, E).to(dtype), dt_raw=(torch.rand(b, L, E, generator=g) * 3.0 - 4.0).to(dtype), z=rn(b, L, E).to(dtype),
+                B=(rn(b, L, G, N) / math.sqrt(N)).to(dtype), C=(rn(b, L, G, N) / math.sqrt(N)).to(dtype),
+                A=-torch.arange(1.0, N + 1.0) * torch.exp(0.3 * rn(E, N)), dt_bias=torch.zeros(E), D=1.0 + 0.3 * rn(E))
