@@ -45,8 +45,9 @@ class StateMap(NamedTuple):
 
 class _On:
     """The device and stream of a call: the tensors' device is made current
-    for it, and what the call allocates is tied to `stream` where that is not
-    the current one.  (The current stream is asked for by its raw handle: a
+    for it, and what the call allocates comes from the memory of `stream`
+    where that is not the current one (a block that was freed on the current
+    one may still be in use there).  (The current stream is asked for by its raw handle: a
     Stream object would cost as much host time as the launch.)"""
     __slots__ = ("device", "handle", "other", "switch", "scratch", "unread")
 
@@ -72,9 +73,12 @@ class _On:
             self.switch.__exit__(*exc)
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            t.record_stream(self.other)
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.other):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        # and the caller may use it here up to the moment it is freed
+        t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def workspace(self, given, need: int):
