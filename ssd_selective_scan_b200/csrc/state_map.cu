@@ -226,7 +226,9 @@ cudaError_t launch_state_map(const StateMapArgs& a, cudaStream_t s)
     const bool alone = a.T <= kFillAlone && entries <= kFillAlone;
     const void* plan = alone ? (const void*)plan_kernel<true> : (const void*)plan_kernel<false>;
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // always the most that a call may need: another thread's smaller call
+        // must not lower it between here and the launch
+        const cudaError_t e = cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMapMaxSlots + 31) / 32 * 4);
         if (e != cudaSuccess) return e;
     }
     if (alone) plan_kernel<true><<<1, kPlanThreads, smem, s>>>(a);
