@@ -16,6 +16,9 @@
  * Notation: E channels, N state elements per channel, G groups of B/C
  * (channel e reads group g = e / (E / G)), T packed tokens, k conv width.
  *
+ * Row counts (b * L; T and nseq together) are at most 2^31 - 65537, else
+ * SSD_ERR_UNSUPPORTED.
+ *
  * The conventions are those of ssd.h (caller-owned device memory, no
  * allocation, no synchronisation, no global state, work enqueued on
  * `stream`, return values), with these shared by the calls below:
@@ -28,7 +31,8 @@
  *     at least G*N (they are usually columns of a projection's rows).
  *   - A [E][N], D [E], dt_bias [E], conv weights (16-byte aligned, as A) and
  *     states are float32;
- *     sums, states and gradients accumulate in float32.  A is expected <= 0.
+ *     sums, states and gradients accumulate in float32.  A is expected <= 0
+ *     (-inf: a state that forgets at once).
  *   - N is a multiple of 4, at most 64 (else SSD_ERR_UNSUPPORTED above 64).
  *
  * Slots.  A serving loop keeps the requests' states (and conv caches) in a
@@ -72,7 +76,10 @@ extern "C" {
  *
  *   lens, ctx  [n] int32    new tokens of each request; tokens it holds
  *   table      [n][max_blocks] int32   block j < ceil(ctx/block_tokens) of
- *                           request r has slot table[r][j]; the rest is ignored
+ *                           request r has slot table[r][j]; the rest is ignored.
+ *                           The call reads the last of these (the state to start
+ *                           from); entries before it are copied as they are, so
+ *                           the slots of earlier states may be given back.
  *   free_list  [nfree] int32, free_head [1] int32   slots free_list[*free_head
  *                           ..] are unused; the call takes as many as the new
  *                           tokens open blocks, in the order of requests and blocks
@@ -81,13 +88,15 @@ extern "C" {
  *   table_out  [n][max_blocks], written: table with the new blocks' slots
  *   free_head_out [1], written: *free_head + slots taken
  *              (each may be its input, for an update in place)
+ *   seq_of, pos_of and slot_of are 16-byte aligned
  *   workspace  ssd_state_map_workspace_bytes(n) bytes, no initial contents
  *   status     device int32, REQUIRED; the caller zeroes it before the call
  * Everything is checked on the device: lengths negative or beyond int32,
  * more than T tokens, a table too narrow, too few free slots, a slot outside
  * [0, nslots), a slot that two requests would write (the same unfinished
- * block twice, a free slot listed twice or still in use by the batch), a
- * slot that one would read while another writes it.  On any of these *status
+ * block twice, a free slot taken twice, a free slot that is also the state
+ * that a request of the batch starts from), a slot that one would start from
+ * while another writes it.  On any of these *status
  * is SSD_ERR_INVALID_ARG, the map is that of a batch without tokens
  * (cu_seqlens zero, the others -1), the table is copied unchanged and no
  * slot is taken.  n == 0 or T == 0 is allowed.  nslots is at most 1500000

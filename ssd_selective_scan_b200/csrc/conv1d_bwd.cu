@@ -33,13 +33,13 @@ constexpr int kRedCols = 32, kRedLanes = 8;
 // fewer CTAs, short ones fill the device where there is little to do.
 inline int tile_rows(int b, int L, int E)
 {
-    const int64_t threads = (int64_t)b * ((L + kTile - 1) / kTile) * (E / 4);
+    const int64_t threads = (int64_t)b * (((int64_t)L + kTile - 1) / kTile) * (E / 4);
     return threads >= 148 * 256 ? kTile : kTileShort;
 }
 inline int tiles_of(int b, int L, int E)
 {
     const int rows = tile_rows(b, L, E);
-    return (L + rows - 1) / rows;
+    return (int)(((int64_t)L + rows - 1) / rows);
 }
 
 template <typename T, int K>

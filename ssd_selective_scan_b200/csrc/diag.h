@@ -19,6 +19,9 @@ struct StateMapArgs {
 };
 constexpr int kMapWsHeader = 64;
 constexpr int kMapMaxSlots = 1500000;
+// Rows and requests of a call: row numbers are ints, and the kernels step up to
+// a tile or a piece past the last row.
+constexpr int64_t kMaxRows = 0x7fffffff - (1 << 16);
 cudaError_t launch_state_map(const StateMapArgs& a, cudaStream_t s);
 
 struct SlotArgs {

@@ -111,7 +111,7 @@ ssd_status_t ssd_state_map(const int32_t* lens, const int32_t* ctx, const int32_
     if (!all_aligned({lens, ctx, table, free_list, free_head, cu_seqlens, init_slot, table_out, free_head_out, workspace, status}, 4) ||
         !all_aligned({seq_of, pos_of, slot_of}, 16))
         return SSD_ERR_INVALID_ARG;
-    if (n > (1 << 24) || (int64_t)n * max_blocks > 0x7fffffffLL || nslots > kMapMaxSlots) return SSD_ERR_UNSUPPORTED;
+    if (n > (1 << 24) || T > kMaxRows || (int64_t)n * max_blocks > 0x7fffffffLL || nslots > kMapMaxSlots) return SSD_ERR_UNSUPPORTED;
     const int64_t entries = (int64_t)n * max_blocks;
     const Range table_in = span(table, entries * 4), table_o = span(table_out, entries * 4);
     const Range head_in = span(free_head, 4), head_o = span(free_head_out, 4);
@@ -149,14 +149,14 @@ ssd_status_t ssd_conv1d_silu_varlen(const void* x, int64_t x_stride, void* out, 
                m.slot, m.init}))
         return SSD_ERR_INVALID_ARG;
     if (k < 2 || k > 4 || E / 512 > 65534) return SSD_ERR_UNSUPPORTED;
-    if ((int64_t)nseq + T > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    if ((int64_t)nseq + T > kMaxRows) return SSD_ERR_UNSUPPORTED;
     if (T == 0 || nseq == 0) return SSD_OK;
     return from_cuda(launch_conv1d_varlen(x, x_stride, out, out_stride, w, bias, cache, sl, T, E, k, dtype == SSD_BF16, stream));
 }
 
 size_t ssd_conv1d_silu_bwd_workspace_bytes(int b, int L, int E, int k)
 {
-    return b <= 0 || L <= 0 || E <= 0 || k <= 0 ? 0 : conv1d_bwd_workspace_bytes(b, L, E, k);
+    return b <= 0 || L <= 0 || (int64_t)b * L > kMaxRows || E <= 0 || k <= 0 ? 0 : conv1d_bwd_workspace_bytes(b, L, E, k);
 }
 
 ssd_status_t ssd_conv1d_silu_bwd(const void* x, const float* w, const float* bias, const void* conv_state,
@@ -177,7 +177,7 @@ ssd_status_t ssd_conv1d_silu_bwd(const void* x, const float* w, const float* bia
                span(workspace, (int64_t)need)},
               {span(x, io), span(w, wb), span(bias, bias ? (int64_t)E * 4 : 0), span(conv_state, conv_state ? cache : 0), span(dout, io)}))
         return SSD_ERR_INVALID_ARG;
-    if (k < 2 || k > 4 || E / 512 > 65534 || (int64_t)b * L > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    if (k < 2 || k > 4 || E / 512 > 65534 || (int64_t)b * L > kMaxRows) return SSD_ERR_UNSUPPORTED;
     if (!tokens) {
         cudaError_t err = cudaMemsetAsync(dw, 0, (size_t)wb, stream);
         if (err == cudaSuccess && dbias) err = cudaMemsetAsync(dbias, 0, (size_t)E * 4, stream);
@@ -201,7 +201,7 @@ ssd_status_t ssd_diag_scan_fwd(const void* u, int64_t u_stride, const void* dt_r
                                void* workspace, size_t workspace_bytes, cudaStream_t stream)
 {
     if (b < 0 || L < 0) return SSD_ERR_INVALID_ARG;
-    if ((int64_t)b * L > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    if ((int64_t)b * L > kMaxRows) return SSD_ERR_UNSUPPORTED;
     DiagArgs a{u, dt_raw, z, B, C, u_stride, dt_stride, z_stride, bc_stride, A, dt_bias, D, init_state, y, final_state,
                b, L, b * L, E, N, G, dtype == SSD_BF16, SlotArgs{}, workspace};
     const ssd_status_t st = check_scan(a, dtype);
@@ -246,14 +246,14 @@ ssd_status_t ssd_diag_scan_fwd_varlen(const void* u, int64_t u_stride, const voi
     if (clash({r.y, span(states, (int64_t)nslots * E * N * 4), span(workspace, (int64_t)need), m.status},
               {r.u, r.dt, r.z, r.B, r.C, r.A, r.bias, r.D, m.cu, m.seq, m.slot, m.init}))
         return SSD_ERR_INVALID_ARG;
-    if ((int64_t)nseq + T > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    if ((int64_t)nseq + T > kMaxRows) return SSD_ERR_UNSUPPORTED;
     if (T == 0 || nseq == 0) return SSD_OK;
     return from_cuda(launch_diag_scan(a, stream));
 }
 
 size_t ssd_diag_scan_bwd_workspace_bytes(int b, int L, int E, int N, int G)
 {
-    if (b <= 0 || L <= 0 || E <= 0 || N <= 0 || N > 64 || G <= 0 || E % G) return 0;
+    if (b <= 0 || L <= 0 || (int64_t)b * L > kMaxRows || E <= 0 || N <= 0 || N > 64 || G <= 0 || E % G) return 0;
     return diag_scan_bwd_workspace_bytes(b, L, E, N, G);
 }
 
@@ -265,7 +265,7 @@ ssd_status_t ssd_diag_scan_bwd(const void* u, int64_t u_stride, const void* dt_r
                                ssd_dtype_t dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream)
 {
     if (b < 0 || L < 0) return SSD_ERR_INVALID_ARG;
-    if ((int64_t)b * L > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    if ((int64_t)b * L > kMaxRows) return SSD_ERR_UNSUPPORTED;
     DiagArgs f{u, dt_raw, z, B, C, u_stride, dt_stride, z_stride, bc_stride, A, dt_bias, D, init_state, nullptr, nullptr,
                b, L, b * L, E, N, G, dtype == SSD_BF16, SlotArgs{}, workspace};
     const ssd_status_t st = check_scan(f, dtype);
@@ -322,6 +322,7 @@ ssd_status_t ssd_diag_state_update(float* states, const void* u, int64_t u_strid
     if (clash({r.y, span(states, (int64_t)nslots * E * N * 4), m.status},
               {r.u, r.dt, r.z, r.B, r.C, r.A, r.bias, r.D, m.cu, m.seq, m.slot, m.init}))
         return SSD_ERR_INVALID_ARG;
+    if (rows > kMaxRows) return SSD_ERR_UNSUPPORTED;
     if (rows == 0) return SSD_OK;
     return from_cuda(launch_diag_update(a, stream));
 }

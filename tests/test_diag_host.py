@@ -183,6 +183,20 @@ def test_scan_bwd_validation():
     assert libssd.ssd_diag_scan_bwd_workspace_bytes(2, 0, 64, 16, 2) == 0 and libssd.ssd_diag_scan_bwd_workspace_bytes(2, 5, 64, 68, 2) == 0
 
 
+def test_row_numbers_stay_ints():
+    """Calls whose last rows lie a tile's step from the end of int are refused
+    (the kernels' row counters would run over)."""
+    T = 2 ** 31 - 9
+    tiny = dict(E=8, N=4, G=1, u_stride=8, dt_stride=8, z_stride=8, bc_stride=4, workspace_bytes=1 << 50)
+    assert smap(T=T) == UNS
+    assert conv(T=T, E=8, x_stride=8, out_stride=8) == UNS
+    assert cbwd(b=1, L=T, E=8, workspace_bytes=1 << 50) == UNS
+    assert scan(b=1, L=T, **tiny) == UNS
+    assert packed(T=T, C=fake(14), **tiny) == UNS
+    assert packed("ssd_diag_state_update", T=T, C=fake(14), **tiny) == UNS
+    assert bwd(b=1, L=T, **tiny) == UNS
+
+
 # ---------------------------------------------------------------------------
 # the references themselves
 
