@@ -8,6 +8,16 @@ namespace ssd {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A log2(e), the factor of dt in a decay's exponent.  Held to finite values: a
+// state that forgets at once (A = -inf) would otherwise turn the rows that
+// fill up a tile, whose dt is 0, into 0 * inf.
+__device__ inline float decay_rate(float A)
+{
+    const float v = A * kLog2e;
+    return v < -3.4028234e38f ? -3.4028234e38f : v;
+}
+__device__ inline float4 decay_rate(float4 A) { return make_float4(decay_rate(A.x), decay_rate(A.y), decay_rate(A.z), decay_rate(A.w)); }
+
 // Packed fp32 pairs: one instruction, each half rounded as the scalar one.
 __device__ inline float2 pk_fma(float2 a, float2 b, float2 c)
 {

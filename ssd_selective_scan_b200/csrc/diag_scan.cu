@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) diag_scan_ke
         st[j] = (int64_t)(e0 + cl[j]) * a.N + 4 * q;
         for (int n = 0; n < 4; ++n) A2[j][n] = h[j][n] = 0.0f;
         if (live[j]) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + st[j]));
-            A2[j][0] = v.x * kLog2e; A2[j][1] = v.y * kLog2e; A2[j][2] = v.z * kLog2e; A2[j][3] = v.w * kLog2e;
+            const float4 v = decay_rate(__ldg(reinterpret_cast<const float4*>(a.A + st[j])));
+            A2[j][0] = v.x; A2[j][1] = v.y; A2[j][2] = v.z; A2[j][3] = v.w;
         }
     }
     auto put4 = [](float* dst, const float (&v)[4]) { *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]); };

@@ -328,8 +328,7 @@ __global__ void __launch_bounds__(kThreads, 3) diag_bwd_kernel(const DiagBwdArgs
             dA[j][k] = make_float2(0.0f, 0.0f);
         }
         if (!live[j]) continue;
-        const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + st[j]));
-        put4(make_float4(v.x * kLog2e, v.y * kLog2e, v.z * kLog2e, v.w * kLog2e), A2[j]);
+        put4(decay_rate(__ldg(reinterpret_cast<const float4*>(a.A + st[j]))), A2[j]);
         // G behind the piece's last row: dfinal, folded over the pieces behind
         if (ba.dfinal) put4(*reinterpret_cast<const float4*>(ba.dfinal + p.r * st_all + st[j]), G[j]);
         for (int64_t i = last; i > p.idx; --i) {

@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kUpdThreads, kUpdCtas) diag_update_kernel(cons
     }
     float A2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (live) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + off));
-        A2[0] = v.x * kLog2e; A2[1] = v.y * kLog2e; A2[2] = v.z * kLog2e; A2[3] = v.w * kLog2e;
+        const float4 v = decay_rate(__ldg(reinterpret_cast<const float4*>(a.A + off)));
+        A2[0] = v.x; A2[1] = v.y; A2[2] = v.z; A2[3] = v.w;
     }
     __syncthreads();
 

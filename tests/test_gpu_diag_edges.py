@@ -33,3 +33,43 @@ def test_results_do_not_take_memory_in_use():
         assert (c == 1).all()
     for y, _ in results:
         assert torch.equal(y, want)
+
+
+NOW = -1e5     # exp(dt A) is 0 in float64 as in float32 (dt >= 0.007: e^-700)
+
+
+def forgetful(p):
+    """(p with every third decay -inf, p with a finite decay of the same effect)"""
+    a, b = dict(p), dict(p)
+    a["A"], b["A"] = p["A"].clone(), p["A"].clone()
+    a["A"].view(-1)[::3] = -float("inf")
+    b["A"].view(-1)[::3] = NOW
+    return a, b
+
+
+@pytest.mark.parametrize("name", ["short", "tile_and_one", "n12", "n64", "cut"])
+def test_scan_forgets_at_once(name):
+    b, L, E, N, G = fwd.DENSE[name]
+    p, q = forgetful(R.scan_inputs((b, L), E, N, G, F32, seed=2, device="cuda"))
+    init = 0.5 * torch.randn(b, E, N, device="cuda")
+    y, fs = ssd.diag_scan_fwd(**p, init_state=init)
+    ry, rf = fwd.dense_ref(q, init)
+    R.close(y, ry, "y")
+    R.close(fs, rf, "final state")
+    one = {k: (v[:, 0] if v is not None and k in bwd.ROWS else v) for k, v in p.items()}
+    st = init.clone()
+    y1 = ssd.diag_state_update(st, one["u"], one["dt_raw"], one["A"], one["B"], one["C"], dt_bias=one["dt_bias"], D=one["D"], z=one["z"])
+    R.close(y1, ry[:, 0], "y of one token")
+
+
+@pytest.mark.parametrize("name", ["short", "tile_and_one", "n12", "n64", "cut"])
+def test_scan_bwd_forgets_at_once(name):
+    p, init, dfinal, dy = bwd.case(name, True, F32, seed=3)
+    p, q = forgetful(p)
+    r = ssd.diag_scan_bwd(**p, dy=dy.cuda(), init_state=init.cuda(), dfinal=dfinal.cuda())
+    d = {k: (v.requires_grad_() if v is not None else None) for k, v in R.f64(q).items()}
+    di = init.double().requires_grad_()
+    bwd.loss(d, di, dfinal.double(), dy.double()).backward()
+    for k, name in bwd.NAMES.items():
+        R.close(r[name], d[k].grad, name)
+    R.close(r["dinit"], di.grad, "dinit")
