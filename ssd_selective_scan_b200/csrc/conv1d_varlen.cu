@@ -169,13 +169,23 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
 
 // Batches of single tokens: a CTA takes SEQS sequences of its channels, so
 // that their taps (64 bytes a thread, against 8 of x) are read once for all
-// and their caches are on the way together.  A sequence of more tokens is
-// walked by the same thread, whole.
+// and their caches are on the way together.  Of a sequence of more tokens the
+// same thread walks the first piece; the pieces behind (a prompt among the
+// single tokens) are the grid's last CTAs', from index `heads`.
 template <typename T, int K, int SEQS>
 __global__ void __launch_bounds__(kThreads)
 conv1d_tokens_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, int64_t os, const float* __restrict__ w,
-                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E)
+                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E, int heads)
 {
+    if ((int)blockIdx.x >= heads) {
+        const int c0 = (blockIdx.y * kThreads + threadIdx.x) * kCpt;
+        Piece p;
+        if (!find_piece_packed(sl.nseq + (int)blockIdx.x - heads, sl, rows, kPiece, K - 2, p) || c0 >= E) return;
+        Taps<K> taps;
+        taps.load(w, bias, c0);
+        walk_piece<T, K>(p, x, xs, out, os, taps, cache, sl, E, c0);
+        return;
+    }
     __shared__ int first[SEQS], count[SEQS], init[SEQS], slot[SEQS];
     if (threadIdx.x < SEQS) {
         const int r = blockIdx.x * SEQS + threadIdx.x;
@@ -226,9 +236,7 @@ conv1d_tokens_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
             if (slot[i] >= 0) now.store(cache + ((int64_t)slot[i] * E + c0) * K);
         } else if (count[i] > 1) {
             Piece p;
-            p.r = blockIdx.x * SEQS + i;
-            p.t0 = p.s0 = first[i];
-            p.t1 = p.s1 = first[i] + count[i];
+            if (!find_piece_packed((int)blockIdx.x * SEQS + i, sl, rows, kPiece, K - 2, p)) continue;
             walk_piece<T, K>(p, x, xs, out, os, taps, cache, sl, E, c0);
         }
     }
@@ -243,8 +251,9 @@ cudaError_t launch_k(const void* x, int64_t xs, void* out, int64_t os, const flo
     const unsigned cols = (unsigned)((E + per - 1) / per);
     if (rows <= 2 * (int64_t)a.nseq) {
         constexpr int SEQS = sizeof(T) == 2 ? 8 : 4;
-        conv1d_tokens_kernel<T, K, SEQS><<<dim3((unsigned)((a.nseq + SEQS - 1) / SEQS), cols), kThreads, 0, s>>>(
-            static_cast<const T*>(x), xs, static_cast<T*>(out), os, w, bias, static_cast<T*>(cache), sl, rows, E);
+        const int heads = (a.nseq + SEQS - 1) / SEQS;
+        conv1d_tokens_kernel<T, K, SEQS><<<dim3((unsigned)(heads + (rows - 1) / kPiece), cols), kThreads, 0, s>>>(
+            static_cast<const T*>(x), xs, static_cast<T*>(out), os, w, bias, static_cast<T*>(cache), sl, rows, E, heads);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)(a.nseq + (rows - 1) / kPiece), cols);

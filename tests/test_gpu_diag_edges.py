@@ -14,6 +14,25 @@ pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 DTYPES = pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 
+# At most two rows to a request, some with many more than one.
+MIXED = {
+    "a_prompt": ([1] * 70 + [100] + [1] * 9 + [0] * 12 + [1] * 5, 16),
+    "prompts": ([0] * 60 + [33, 1, 64, 2, 32] + [0] * 20, 7),
+    "in_one_block": ([1] * 100 + [95], 4096),
+    "block_of_one": ([1] * 40 + [35] + [0] * 8, 1),
+}
+
+
+@DTYPES
+@pytest.mark.parametrize("k", [2, 3, 4])
+@pytest.mark.parametrize("name", sorted(MIXED))
+def test_conv_prompts_among_single_tokens(name, k, dtype, monkeypatch):
+    lens, bs = MIXED[name]
+    assert sum(lens) + 3 <= 2 * len(lens)
+    monkeypatch.setitem(fwd.CONV_BATCHES, name, (lens, [(5 * i) % 37 for i in range(len(lens))], bs))
+    fwd.test_conv_varlen(name, k, dtype)
+
+
 def test_results_do_not_take_memory_in_use():
     """A result on another stream is not laid into a block that was freed on
     the current one while work there still reads it."""
