@@ -92,3 +92,16 @@ def test_scan_bwd_forgets_at_once(name):
     for k, name in bwd.NAMES.items():
         R.close(r[name], d[k].grad, name)
     R.close(r["dinit"], di.grad, "dinit")
+
+
+def test_state_map_reads_the_last_state_only():
+    """The slots of a request's earlier blocks may be given back and used anew."""
+    q = R.batch([4, 6], [9, 3], 4, seed=1, spare=4)
+    old = q["table"][0, :2].copy()
+    q["free"] = np.concatenate([old[:1], q["free"]])      # block 0's slot is the first to be taken
+    q["table"][0, 1] = -1                                   # block 1's belongs to nobody
+    T = 11
+    st = fwd.zero_status()
+    m = fwd.call_map(q, T, st)
+    fwd.assert_map(m, R.ref_map(q, T))
+    assert st.item() == 0
