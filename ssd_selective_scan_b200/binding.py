@@ -14,6 +14,7 @@ import threading
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libssd.so")
+PYCALL_PATH = os.path.join(PKG_DIR, "_pycall.so")
 
 # ssd_status_t
 SSD_OK = 0
@@ -104,6 +105,16 @@ def load() -> ctypes.CDLL:
                 fn.argtypes = args
             _lib = lib
     return _lib
+
+
+def load_pycall():
+    """The extension module of csrc/pycall.cpp.  Raises if it has not been built."""
+    load()
+    try:
+        from . import _pycall
+    except ImportError as e:
+        raise RuntimeError(f"{PYCALL_PATH}: {e}; build it with `python -m ssd_selective_scan_b200.build` (there is no fallback path)") from e
+    return _pycall
 
 
 def status_string(status: int) -> str:

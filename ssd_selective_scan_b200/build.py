@@ -1,19 +1,23 @@
-"""Build libssd.so in-tree from csrc/*.cu for sm_100a (B200).
+"""Build libssd.so in-tree from csrc/*.cu for sm_100a (B200), and the Python
+extension _pycall.so from csrc/pycall.cpp.
 
     python -m ssd_selective_scan_b200.build [--force] [-v]
 
 Each translation unit is compiled by nvcc into _build/ (in parallel), then
 linked into ssd_selective_scan_b200/libssd.so with the static CUDA runtime.
-Only sm_100a SASS is generated: the library targets B200 alone.
+Only sm_100a SASS is generated: the library targets B200 alone.  The extension
+is host code against torch's and Python's headers, linked to libssd.so beside it.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +25,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd.so")
+PYCALL_SRC = os.path.join(CSRC, "pycall.cpp")
+PYCALL = os.path.join(PKG, "_pycall.so")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -37,11 +44,28 @@ def _deps():
         sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
 
 
+def _fresh(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _fresh(LIB, _deps())
+
+
+def _build_pycall(verbose: bool) -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = PYCALL + f".tmp{os.getpid()}"
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"), PYCALL_SRC, "-o", tmp,
+           "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed on {PYCALL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYCALL)
 
 
 def _compile(src: str, verbose: bool, extra) -> str:
@@ -58,8 +82,14 @@ def _compile(src: str, verbose: bool, extra) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+    if force or not up_to_date():
+        _build_lib(verbose, ptxas_info)
+    if force or not _fresh(PYCALL, [PYCALL_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.join(INCLUDE, "ssd_diag.h"), os.path.abspath(__file__)]):
+        _build_pycall(verbose)
+    return LIB
+
+
+def _build_lib(verbose: bool, ptxas_info: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
@@ -70,7 +100,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
-    return LIB
 
 
 def main(argv=None):

@@ -27,6 +27,17 @@ import torch
 from . import binding as libssd
 from .layer import _dtype_code, _ptr
 
+# The extension that checks the tensors and makes the calls (csrc/pycall.cpp),
+# loaded with the first call; and its checks of a contiguous tensor, of evenly
+# spaced rows and of B and C, each giving what the call takes.
+_native = _dense = _rows = _bc = None
+
+
+def _load():
+    global _native, _dense, _rows, _bc
+    _native = libssd.load_pycall()
+    _dense, _rows, _bc = _native.dense, _native.rows, _native.bc
+
 
 class StateMap(NamedTuple):
     """Where a packed batch's requests, rows and states are (device tensors;
@@ -54,6 +65,8 @@ class _On:
     def __init__(self, like: torch.Tensor, stream):
         if not like.is_cuda:
             raise ValueError("CUDA tensors expected")
+        if _native is None:
+            _load()
         self.device = like.device
         index = like.get_device()
         if stream is not None and stream.device != self.device:
@@ -74,9 +87,9 @@ class _On:
 
     def empty(self, shape, dtype):
         if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return _native.empty(shape, dtype, self.device)
         with torch.cuda.stream(self.other):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
+            t = _native.empty(shape, dtype, self.device)
         # and the caller may use it here up to the moment it is freed
         t.record_stream(torch.cuda.current_stream(self.device))
         return t
@@ -86,63 +99,10 @@ class _On:
         if given is None:
             if not need:
                 return None, 0
-            given = self.scratch = self.empty(need, torch.uint8)
+            given = self.scratch = self.empty((need,), torch.uint8)
         elif given.device != self.device or not given.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
         return given.data_ptr(), given.numel() * given.element_size()
-
-
-def _dense(t, name, dtype, shape, device):
-    """The pointer of a contiguous tensor of this type and shape (None passes)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t.data_ptr()
-
-
-def _rows(t, name, lead, E, like) -> tuple[int | None, int]:
-    """(pointer, row stride) of a [*lead, E] tensor whose rows are evenly
-    spaced and dense."""
-    if t is None:
-        return None, E
-    if t.shape != (*lead, E) or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {(*lead, E)} on {like.device}")
-    return t.data_ptr(), _row_stride(t, t.stride(), name, lead, E)
-
-
-def _row_stride(t, st, name, lead, E) -> int:
-    # a dimension of one row says nothing about the spacing
-    L = lead[-1]
-    if st[-1] != 1 and E > 1 and t.numel():
-        raise ValueError(f"{name} must have dense rows")
-    if len(lead) == 1:
-        return st[0] if L > 1 else E
-    if not t.numel():
-        return E
-    if lead[0] > 1 and L > 1 and st[0] != L * st[1]:
-        raise ValueError(f"{name} must have evenly spaced rows")
-    return st[1] if L > 1 else st[0] if lead[0] > 1 else E
-
-
-def _bc(B, C, lead, like) -> tuple[int | None, int | None, int, int, int]:
-    """B, C [*lead, G, N] as (pointer, pointer, row stride, G, N)."""
-    shape = B.shape
-    if shape != C.shape or len(shape) != len(lead) + 2 or shape[:-2] != lead:
-        raise ValueError(f"B and C must share the shape {(*lead, 'G', 'N')}")
-    G, N = shape[-2], shape[-1]
-    rs = None
-    for t, name in ((B, "B"), (C, "C")):
-        if t.dtype != like.dtype or t.device != like.device:
-            raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
-        st = t.stride()
-        if G > 1 and st[-2] != N and t.numel():
-            raise ValueError(f"{name}: dense (G, N) rows expected")
-        s = _row_stride(t, (*st[:-2], st[-1]), name, lead, G * N)
-        if rs is not None and s != rs:
-            raise ValueError("B and C must share one row stride")
-        rs = s
-    return B.data_ptr(), C.data_ptr(), rs, G, N
 
 
 def _map(m: StateMap, T: int, device):
@@ -155,7 +115,7 @@ def _map(m: StateMap, T: int, device):
 def _status(status, on):
     if status is None:
         # of the call's own: nobody reads it, but the kernels need the place
-        status = on.unread = on.empty(1, torch.int32)
+        status = on.unread = on.empty((1,), torch.int32)
     return _dense(status, "status", torch.int32, (1,), on.device)
 
 
@@ -183,13 +143,14 @@ def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_l
             # one allocation for the int32 parts (seq_of and pos_of on 16
             # bytes) and the workspace
             n4, T4 = (n + 4) // 4 * 4, (T + 3) // 4 * 4
-            parts = on.empty(n4 + 2 * T4 + n4 + n * mb + 1 + (0 if workspace is not None else scratch), i32)
-            cu, _, seq, _, pos, _, init, _, tab, head, _ = parts.split_with_sizes(
-                (n + 1, n4 - n - 1, T, T4 - T, T, T4 - T, n, n4 - n, n * mb, 1, 0 if workspace is not None else scratch))
-            out = StateMap(cu, seq, pos, on.empty(T, torch.int64), init, tab.view(n, mb), head, block_tokens)
+            at_pos, at_init, at_table = n4 + T4, n4 + 2 * T4, 2 * n4 + 2 * T4
+            at_head = at_table + n * mb
+            parts = on.empty((at_head + 1 + (0 if workspace is not None else scratch),), i32)
+            part = _native.part
+            out = StateMap(part(parts, (n + 1,), 0), part(parts, (T,), n4), part(parts, (T,), at_pos), on.empty((T,), torch.int64),
+                           part(parts, (n,), at_init), part(parts, (n, mb), at_table), part(parts, (1,), at_head), block_tokens)
             at = parts.data_ptr()
-            ptrs = (at, at + 4 * n4, at + 4 * (n4 + T4), out.slot_of.data_ptr(), at + 4 * (n4 + 2 * T4), at + 4 * (2 * n4 + 2 * T4),
-                    at + 4 * (2 * n4 + 2 * T4 + n * mb))
+            ptrs = (at, at + 4 * n4, at + 4 * at_pos, out.slot_of.data_ptr(), at + 4 * at_init, at + 4 * at_table, at + 4 * at_head)
             if workspace is None:
                 wp, wb = ptrs[-1] + 4, 4 * scratch
         else:
@@ -201,7 +162,7 @@ def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_l
         if workspace is not None:
             wp, wb = on.workspace(workspace, 4 * scratch)
         nfree = free_list.numel()
-        st = libssd.ssd_state_map(
+        st = _native.ssd_state_map(
             _dense(lens, "lens", i32, (n,), dev), _dense(ctx, "ctx", i32, (n,), dev), _dense(table, "table", i32, (n, mb), dev),
             _dense(free_list, "free_list", i32, (nfree,), dev), _dense(free_head, "free_head", i32, (1,), dev),
             n, mb, nfree, T, block_tokens, nslots, *ptrs, wp, wb, _status(status, on), on.handle)
@@ -227,10 +188,10 @@ def conv1d_silu_varlen(x: torch.Tensor, w: torch.Tensor, cache: torch.Tensor, m:
         op, os_ = _rows(out, "out", (T,), E, x)
         cu, seq, slot, init, n = _map(m, T, dev)
         nslots = cache.shape[0]
-        st = libssd.ssd_conv1d_silu_varlen(xp, xs, op, os_, _dense(w, "w", torch.float32, (E, k), dev),
-                                           _dense(bias, "bias", torch.float32, (E,), dev),
-                                           _dense(cache, "cache", x.dtype, (nslots, E, k), dev), cu, seq, slot, init, n, T, E, k,
-                                           m.block_tokens, nslots, _dtype_code(x), _status(status, on), on.handle)
+        st = _native.ssd_conv1d_silu_varlen(xp, xs, op, os_, _dense(w, "w", torch.float32, (E, k), dev),
+                                            _dense(bias, "bias", torch.float32, (E,), dev),
+                                            _dense(cache, "cache", x.dtype, (nslots, E, k), dev), cu, seq, slot, init, n, T, E, k,
+                                            m.block_tokens, nslots, _dtype_code(x), _status(status, on), on.handle)
         libssd.check("ssd_conv1d_silu_varlen", st)
     return out
 
@@ -248,13 +209,13 @@ def conv1d_silu_bwd(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, bias: 
     f32 = torch.float32
     with _On(x, stream) as on:
         dev = on.device
-        r = dict(dx=on.empty((b, L, E), x.dtype), dw=on.empty((E, k), f32), dbias=None if bias is None else on.empty(E, f32),
+        r = dict(dx=on.empty((b, L, E), x.dtype), dw=on.empty((E, k), f32), dbias=None if bias is None else on.empty((E,), f32),
                  dconv_state=None if conv_state is None else on.empty((b, E, k), x.dtype))
-        wp, wb = on.workspace(workspace, int(libssd.ssd_conv1d_silu_bwd_workspace_bytes(b, L, E, k)))
-        st = libssd.ssd_conv1d_silu_bwd(_dense(x, "x", x.dtype, (b, L, E), dev), _dense(w, "w", f32, (E, k), dev),
-                                        _dense(bias, "bias", f32, (E,), dev), _dense(conv_state, "conv_state", x.dtype, (b, E, k), dev),
-                                        _dense(dout, "dout", x.dtype, (b, L, E), dev), _ptr(r["dx"]), _ptr(r["dw"]), _ptr(r["dbias"]),
-                                        _ptr(r["dconv_state"]), b, L, E, k, _dtype_code(x), wp, wb, on.handle)
+        wp, wb = on.workspace(workspace, _native.ssd_conv1d_silu_bwd_workspace_bytes(b, L, E, k))
+        st = _native.ssd_conv1d_silu_bwd(_dense(x, "x", x.dtype, (b, L, E), dev), _dense(w, "w", f32, (E, k), dev),
+                                         _dense(bias, "bias", f32, (E,), dev), _dense(conv_state, "conv_state", x.dtype, (b, E, k), dev),
+                                         _dense(dout, "dout", x.dtype, (b, L, E), dev), _ptr(r["dx"]), _ptr(r["dw"]), _ptr(r["dbias"]),
+                                         _ptr(r["dconv_state"]), b, L, E, k, _dtype_code(x), wp, wb, on.handle)
         libssd.check("ssd_conv1d_silu_bwd", st)
     return r
 
@@ -289,12 +250,12 @@ def diag_scan_fwd(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: tor
         up, us = _rows(u, "u", (b, L), E, u)
         dp, ds = _rows(dt_raw, "dt_raw", (b, L), E, u)
         zp, zs = _rows(z, "z", (b, L), E, u)
-        wp, wb = on.workspace(workspace, int(libssd.ssd_diag_scan_workspace_bytes(b, b * L, E, N, G)))
-        st = libssd.ssd_diag_scan_fwd(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
-                                      _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
-                                      _dense(init_state, "init_state", f32, (b, E, N), dev), _dense(y, "y", u.dtype, (b, L, E), dev),
-                                      _dense(final_state, "final_state", f32, (b, E, N), dev), b, L, E, N, G, _dtype_code(u), wp, wb,
-                                      on.handle)
+        wp, wb = on.workspace(workspace, _native.ssd_diag_scan_workspace_bytes(b, b * L, E, N, G))
+        st = _native.ssd_diag_scan_fwd(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
+                                       _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
+                                       _dense(init_state, "init_state", f32, (b, E, N), dev), _dense(y, "y", u.dtype, (b, L, E), dev),
+                                       _dense(final_state, "final_state", f32, (b, E, N), dev), b, L, E, N, G, _dtype_code(u), wp, wb,
+                                       on.handle)
         libssd.check("ssd_diag_scan_fwd", st)
     return y, final_state
 
@@ -320,12 +281,12 @@ def diag_scan_fwd_varlen(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor,
         zp, zs = _rows(z, "z", (T,), E, u)
         cu, seq, slot, init, n = _map(m, T, dev)
         nslots = states.shape[0]
-        wp, wb = on.workspace(workspace, int(libssd.ssd_diag_scan_workspace_bytes(n, T, E, N, G)))
-        st = libssd.ssd_diag_scan_fwd_varlen(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
-                                             _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
-                                             _dense(states, "states", f32, (nslots, E, N), dev), _dense(y, "y", u.dtype, (T, E), dev),
-                                             cu, seq, slot, init, n, T, E, N, G, m.block_tokens, nslots, _dtype_code(u), wp, wb,
-                                             _status(status, on), on.handle)
+        wp, wb = on.workspace(workspace, _native.ssd_diag_scan_workspace_bytes(n, T, E, N, G))
+        st = _native.ssd_diag_scan_fwd_varlen(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
+                                              _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
+                                              _dense(states, "states", f32, (nslots, E, N), dev), _dense(y, "y", u.dtype, (T, E), dev),
+                                              cu, seq, slot, init, n, T, E, N, G, m.block_tokens, nslots, _dtype_code(u), wp, wb,
+                                              _status(status, on), on.handle)
         libssd.check("ssd_diag_scan_fwd_varlen", st)
     return y
 
@@ -350,15 +311,15 @@ def diag_scan_bwd(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: tor
         dp, ds = _rows(dt_raw, "dt_raw", (b, L), E, u)
         zp, zs = _rows(z, "z", (b, L), E, u)
         io, bc = (lambda: on.empty((b, L, E), u.dtype)), (lambda: on.empty((b, L, G, N), u.dtype))
-        r = dict(du=io(), ddt_raw=io(), dz=None if z is None else io(), dB=bc(), dC=bc(), dA=on.empty((E, N), f32), dD=on.empty(E, f32),
-                 ddt_bias=on.empty(E, f32), dinit=on.empty((b, E, N), f32) if want_dinit else None)
-        wp, wb = on.workspace(workspace, int(libssd.ssd_diag_scan_bwd_workspace_bytes(b, L, E, N, G)))
-        st = libssd.ssd_diag_scan_bwd(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
-                                      _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
-                                      _dense(init_state, "init_state", f32, (b, E, N), dev), _dense(dy, "dy", u.dtype, (b, L, E), dev),
-                                      _dense(dfinal, "dfinal", f32, (b, E, N), dev), _ptr(r["du"]), _ptr(r["ddt_raw"]), _ptr(r["dz"]),
-                                      _ptr(r["dB"]), _ptr(r["dC"]), _ptr(r["dA"]), _ptr(r["dD"]), _ptr(r["ddt_bias"]), _ptr(r["dinit"]),
-                                      b, L, E, N, G, _dtype_code(u), wp, wb, on.handle)
+        r = dict(du=io(), ddt_raw=io(), dz=None if z is None else io(), dB=bc(), dC=bc(), dA=on.empty((E, N), f32), dD=on.empty((E,), f32),
+                 ddt_bias=on.empty((E,), f32), dinit=on.empty((b, E, N), f32) if want_dinit else None)
+        wp, wb = on.workspace(workspace, _native.ssd_diag_scan_bwd_workspace_bytes(b, L, E, N, G))
+        st = _native.ssd_diag_scan_bwd(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
+                                       _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
+                                       _dense(init_state, "init_state", f32, (b, E, N), dev), _dense(dy, "dy", u.dtype, (b, L, E), dev),
+                                       _dense(dfinal, "dfinal", f32, (b, E, N), dev), _ptr(r["du"]), _ptr(r["ddt_raw"]), _ptr(r["dz"]),
+                                       _ptr(r["dB"]), _ptr(r["dC"]), _ptr(r["dA"]), _ptr(r["dD"]), _ptr(r["ddt_bias"]), _ptr(r["dinit"]),
+                                       b, L, E, N, G, _dtype_code(u), wp, wb, on.handle)
         libssd.check("ssd_diag_scan_bwd", st)
     return r
 
@@ -389,9 +350,9 @@ def diag_state_update(states: torch.Tensor, u: torch.Tensor, dt_raw: torch.Tenso
             bs = m.block_tokens
             sp = _status(status, on)
         nslots = states.shape[0]
-        st = libssd.ssd_diag_state_update(_dense(states, "states", f32, (nslots, E, N), dev), up, us, dp, ds, zp, zs, pB, pC, bcs,
-                                          _dense(A, "A", f32, (E, N), dev), _dense(dt_bias, "dt_bias", f32, (E,), dev),
-                                          _dense(D, "D", f32, (E,), dev), _dense(y, "y", u.dtype, (T, E), dev), cu, seq, slot, init, n,
-                                          T, E, N, G, bs, nslots, _dtype_code(u), sp, on.handle)
+        st = _native.ssd_diag_state_update(_dense(states, "states", f32, (nslots, E, N), dev), up, us, dp, ds, zp, zs, pB, pC, bcs,
+                                           _dense(A, "A", f32, (E, N), dev), _dense(dt_bias, "dt_bias", f32, (E,), dev),
+                                           _dense(D, "D", f32, (E,), dev), _dense(y, "y", u.dtype, (T, E), dev), cu, seq, slot, init, n,
+                                           T, E, N, G, bs, nslots, _dtype_code(u), sp, on.handle)
         libssd.check("ssd_diag_state_update", st)
     return y
