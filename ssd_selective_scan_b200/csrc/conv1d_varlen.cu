@@ -21,6 +21,7 @@ constexpr int kThreads = 128;
 constexpr int kCpt = 4;      // channels per thread
 constexpr int kPiece = 32;   // rows per piece
 constexpr int kGroup = 8;    // rows loaded together
+constexpr int kGroupFew = 2; // the same where long sequences are few: their registers would cost every CTA
 
 // A thread's taps and bias.
 template <int K> struct Taps {
@@ -44,8 +45,9 @@ template <int K> struct Taps {
     }
 };
 
-// The rows of one piece for the thread's 4 channels from c0.
-template <typename T, int K>
+// The rows of one piece for the thread's 4 channels from c0, GROUP
+// of them loaded together.
+template <typename T, int K, int GROUP>
 __device__ inline void walk_piece(const Piece& p, const T* x, int64_t xs, T* out, int64_t os, const Taps<K>& taps, T* cache,
                                   const Slots& sl, int E, int c0)
 {
@@ -133,13 +135,13 @@ __device__ inline void walk_piece(const Piece& p, const T* x, int64_t xs, T* out
         if (slot >= 0) keep_state((int)t, slot);
     }
 
-    for (int tb = p.t0; tb < p.t1; tb += kGroup) {
-        Row4<T> raw[kGroup];
+    for (int tb = p.t0; tb < p.t1; tb += GROUP) {
+        Row4<T> raw[GROUP];
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
+        for (int u = 0; u < GROUP; ++u)
             if (tb + u < p.t1) raw[u].load(xb + (int64_t)(tb + u) * xs);
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
+        for (int u = 0; u < GROUP; ++u) {
             if (tb + u < p.t1) {
                 raw[u].get(hist[K - 1]);
                 float o[kCpt];
@@ -164,59 +166,61 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
     if (!find_piece_packed(blockIdx.x, sl, rows, kPiece, K - 2, p) || c0 >= E) return;
     Taps<K> taps;
     taps.load(w, bias, c0);
-    walk_piece<T, K>(p, x, xs, out, os, taps, cache, sl, E, c0);
+    walk_piece<T, K, kGroup>(p, x, xs, out, os, taps, cache, sl, E, c0);
 }
 
 // Batches of single tokens: a CTA takes SEQS sequences of its channels, so
 // that their taps (64 bytes a thread, against 8 of x) are read once for all
-// and their caches are on the way together.  Of a sequence of more tokens the
-// same thread walks the first piece; the pieces behind (a prompt among the
-// single tokens) are the grid's last CTAs', from index `heads`.
+// and their caches are on the way together.  Sequences of more tokens (a
+// prompt among the single tokens) are walked in pieces: the first by the CTA
+// that has the sequence, those behind by the CTAs in turn, one to each at most,
+// as there are at most two rows to a sequence.
+// (The CTAs an SM must hold are set by what single tokens need; the walk of a
+// long sequence spills 20 registers for it.)
 template <typename T, int K, int SEQS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4)
 conv1d_tokens_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, int64_t os, const float* __restrict__ w,
-                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E, int heads)
+                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E)
 {
-    if ((int)blockIdx.x >= heads) {
-        const int c0 = (blockIdx.y * kThreads + threadIdx.x) * kCpt;
-        Piece p;
-        if (!find_piece_packed(sl.nseq + (int)blockIdx.x - heads, sl, rows, kPiece, K - 2, p) || c0 >= E) return;
-        Taps<K> taps;
-        taps.load(w, bias, c0);
-        walk_piece<T, K>(p, x, xs, out, os, taps, cache, sl, E, c0);
-        return;
-    }
-    __shared__ int first[SEQS], count[SEQS], init[SEQS], slot[SEQS];
+    static_assert(2 * SEQS <= kPiece, "a CTA has one later piece at most");
+    __shared__ int first[SEQS], count[SEQS], init[SEQS], slot[SEQS], later;
     if (threadIdx.x < SEQS) {
         const int r = blockIdx.x * SEQS + threadIdx.x;
-        int n = 0, in = -1, to = -1, s0 = 0;
+        int n = 0, in = -1, s0 = 0;
         if (r < sl.nseq) {
             s0 = sl.cu[r];
             const int s1 = sl.cu[r + 1];
             in = sl.init_slot[r];
             if (s0 < 0 || s1 < s0 || s1 > rows || in >= sl.nslots) flag_invalid(sl.status);
             else n = s1 - s0;
-            if (n == 1) to = slot_at(sl, sl.slot_of[s0]);
         }
         first[threadIdx.x] = s0;
         count[threadIdx.x] = n;
         init[threadIdx.x] = in;
-        slot[threadIdx.x] = to;
+    } else if (threadIdx.x == 32) {   // does a piece begin at this CTA's row? (find_piece_packed checks the rest)
+        const int64_t at = ((int64_t)blockIdx.x + 1) * kPiece;
+        const int r = at < rows ? sl.seq_of[at] : -1;
+        later = r >= 0 && !(r < sl.nseq && at - sl.cu[r] <= K - 2);
     }
-    __syncthreads();
+    // what needs no lookup is on its way before the lookups are back, and the
+    // slots to write are looked up while the inputs are on theirs
     const int c0 = (blockIdx.y * kThreads + threadIdx.x) * kCpt;
-    if (c0 >= E) return;
+    const bool live = c0 < E;
+    Taps<K> taps;
+    if (live) taps.load(w, bias, c0);
+    __syncthreads();
     Cache4<T, K> old[SEQS];
     Row4<T> in[SEQS];
 #pragma unroll
     for (int i = 0; i < SEQS; ++i)
-        if (count[i] == 1) {
+        if (live && count[i] == 1) {
             in[i].load(x + (int64_t)first[i] * xs + c0);
             if (init[i] >= 0) old[i].load(cache + ((int64_t)init[i] * E + c0) * K);
             else old[i].zero();
         }
-    Taps<K> taps;
-    taps.load(w, bias, c0);
+    if (threadIdx.x < SEQS && count[threadIdx.x] == 1) slot[threadIdx.x] = slot_at(sl, sl.slot_of[first[threadIdx.x]]);
+    __syncthreads();
+    if (!live) return;
 #pragma unroll
     for (int i = 0; i < SEQS; ++i) {
         if (count[i] == 1) {
@@ -234,11 +238,14 @@ conv1d_tokens_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
 #pragma unroll
                 for (int c = 0; c < kCpt; ++c) now.set(c, j, v[j][c]);
             if (slot[i] >= 0) now.store(cache + ((int64_t)slot[i] * E + c0) * K);
-        } else if (count[i] > 1) {
-            Piece p;
-            if (!find_piece_packed((int)blockIdx.x * SEQS + i, sl, rows, kPiece, K - 2, p)) continue;
-            walk_piece<T, K>(p, x, xs, out, os, taps, cache, sl, E, c0);
         }
+    }
+#pragma unroll 1
+    for (int i = 0; i <= SEQS; ++i) {
+        if (i < SEQS ? count[i] <= 1 : !later) continue;
+        Piece p;
+        if (find_piece_packed(i < SEQS ? (int)blockIdx.x * SEQS + i : sl.nseq + (int)blockIdx.x, sl, rows, kPiece, K - 2, p))
+            walk_piece<T, K, kGroupFew>(p, x, xs, out, os, taps, cache, sl, E, c0);
     }
 }
 
@@ -250,10 +257,12 @@ cudaError_t launch_k(const void* x, int64_t xs, void* out, int64_t os, const flo
     const int per = kThreads * kCpt;
     const unsigned cols = (unsigned)((E + per - 1) / per);
     if (rows <= 2 * (int64_t)a.nseq) {
-        constexpr int SEQS = sizeof(T) == 2 ? 8 : 4;
-        const int heads = (a.nseq + SEQS - 1) / SEQS;
-        conv1d_tokens_kernel<T, K, SEQS><<<dim3((unsigned)(heads + (rows - 1) / kPiece), cols), kThreads, 0, s>>>(
-            static_cast<const T*>(x), xs, static_cast<T*>(out), os, w, bias, static_cast<T*>(cache), sl, rows, E, heads);
+        // 256 tokens of 8192 bf16 channels 14.7 us (2.9 TB/s), 512 24.8, 256 of 2560
+        // 5.1, 16 of 4096 3.6; 4 sequences to a CTA, 4 CTAs an SM: 14.7, 26.3, 5.5,
+        // 4.4; 8 and 3: 20.2, 30.6, 7.7, 6.7.  256 tokens of 8192 f32 channels 24.3.
+        constexpr int SEQS = 2;
+        conv1d_tokens_kernel<T, K, SEQS><<<dim3((unsigned)((a.nseq + SEQS - 1) / SEQS), cols), kThreads, 0, s>>>(
+            static_cast<const T*>(x), xs, static_cast<T*>(out), os, w, bias, static_cast<T*>(cache), sl, rows, E);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)(a.nseq + (rows - 1) / kPiece), cols);

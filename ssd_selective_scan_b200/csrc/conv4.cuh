@@ -30,7 +30,7 @@ template <> struct Row4<__nv_bfloat16> {
 };
 
 // The cache of one thread's channels in one slot: 4 * K adjacent elements,
-// moved as 8-byte (bf16) or 16-byte (f32) vectors.
+// moved as 16-byte vectors where they are a multiple of that, else 8-byte ones.
 template <typename T, int K> struct Cache4 {
     static constexpr int kWords = 4 * K * (int)sizeof(T) / 4;
     uint32_t w[kWords];
@@ -41,17 +41,31 @@ template <typename T, int K> struct Cache4 {
     }
     __device__ void load(const T* p)
     {
+        if constexpr (kWords % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < kWords / 2; ++i) {
-            const uint2 q = reinterpret_cast<const uint2*>(p)[i];
-            w[2 * i] = q.x;
-            w[2 * i + 1] = q.y;
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 2; ++i) {
+                const uint2 q = reinterpret_cast<const uint2*>(p)[i];
+                w[2 * i] = q.x;
+                w[2 * i + 1] = q.y;
+            }
         }
     }
     __device__ void store(T* p) const
     {
+        if constexpr (kWords % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < kWords / 2; ++i) reinterpret_cast<uint2*>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 2; ++i) reinterpret_cast<uint2*>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+        }
     }
     __device__ float get(int c, int j) const { return io<T>::word_get(w, c * K + j); }
     __device__ void set(int c, int j, float v) { io<T>::word_set(w, c * K + j, v); }
