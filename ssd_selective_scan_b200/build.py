@@ -58,7 +58,7 @@ def _build_pycall(verbose: bool) -> None:
     tmp = PYCALL + f".tmp{os.getpid()}"
     cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"), PYCALL_SRC, "-o", tmp,
-           "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
            "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)

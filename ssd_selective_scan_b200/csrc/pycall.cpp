@@ -13,6 +13,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Device.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -68,6 +70,13 @@ bool has_shape(const at::Tensor& t, const int64_t* v, int n)
     return true;
 }
 
+void bad_dense(PyObject* name, PyObject* dtype, PyObject* shape, PyObject* device)
+{
+    PyObject* plain = PySequence_Tuple(shape);   // a torch.Size prints as a tuple
+    if (plain) PyErr_Format(PyExc_ValueError, "%U must be a contiguous %S tensor of shape %S on %S", name, dtype, plain, device);
+    Py_XDECREF(plain);
+}
+
 PyObject* pointer(const at::Tensor& t) { return PyLong_FromVoidPtr(t.data_ptr()); }
 
 // dense(t, name, dtype, shape, device): the pointer of a contiguous tensor of
@@ -87,9 +96,7 @@ PyObject* dense(PyObject*, PyObject* const* a, Py_ssize_t n)
     }
     if (t->scalar_type() != reinterpret_cast<THPDtype*>(a[2])->scalar_type || t->device() != reinterpret_cast<THPDevice*>(a[4])->device ||
         !has_shape(*t, dims, nd) || !t->is_contiguous()) {
-        PyObject* shape = PySequence_Tuple(a[3]);   // a torch.Size prints as a tuple
-        if (shape) PyErr_Format(PyExc_ValueError, "%U must be a contiguous %S tensor of shape %S on %S", a[1], a[2], shape, a[4]);
-        Py_XDECREF(shape);
+        bad_dense(a[1], a[2], a[3], a[4]);
         return nullptr;
     }
     return pointer(*t);
@@ -194,6 +201,90 @@ PyObject* bc(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// where(like): (device, raw handle of its current stream, whether it is the
+// current device) of a CUDA tensor
+PyObject* where(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (!arity("where", n, 1)) return nullptr;
+    if (!THPVariable_Check(a[0])) {
+        PyErr_SetString(PyExc_TypeError, "a tensor expected");
+        return nullptr;
+    }
+    const at::Tensor& t = THPVariable_Unpack(a[0]);
+    if (!t.is_cuda()) {
+        PyErr_SetString(PyExc_ValueError, "CUDA tensors expected");
+        return nullptr;
+    }
+    const c10::Device dev = t.device();
+    const auto stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    return Py_BuildValue("(NKN)", THPDevice_New(dev), (unsigned long long)(uintptr_t)stream,
+                         PyBool_FromLong(c10::cuda::current_device() == dev.index()));
+    END_HANDLE_TH_ERRORS
+}
+
+// map_in(cu_seqlens, seq_of, slot_of, init_slot, T, device): the pointers of a
+// state map's parts for T rows, and its requests
+PyObject* map_in(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (!arity("map_in", n, 6)) return nullptr;
+    static const char* const names[] = {"cu_seqlens", "seq_of", "slot_of", "init_slot"};
+    const at::Tensor* t[4];
+    for (int i = 0; i < 4; ++i) {
+        if (!THPVariable_Check(a[i])) return PyErr_Format(PyExc_TypeError, "%s must be a tensor", names[i]);
+        t[i] = &THPVariable_Unpack(a[i]);
+    }
+    const int64_t T = PyLong_AsLongLong(a[4]);
+    if (T == -1 && PyErr_Occurred()) return nullptr;
+    if (!THPDevice_Check(a[5])) return PyErr_Format(PyExc_TypeError, "map_in: a device expected");
+    const int64_t nseq = t[0]->numel() - 1;
+    const int64_t len[] = {nseq + 1, T, T, nseq};
+    for (int i = 0; i < 4; ++i) {
+        const auto type = i == 2 ? at::ScalarType::Long : at::ScalarType::Int;
+        if (len[i] < 0 || t[i]->scalar_type() != type || t[i]->device() != reinterpret_cast<THPDevice*>(a[5])->device ||
+            !has_shape(*t[i], &len[i], 1) || !t[i]->is_contiguous())
+            return PyErr_Format(PyExc_ValueError, "%s must be a contiguous torch.%s tensor of shape (%lld,) on %S", names[i],
+                                i == 2 ? "int64" : "int32", (long long)len[i], a[5]);
+    }
+    return Py_BuildValue("(NNNNL)", pointer(*t[0]), pointer(*t[1]), pointer(*t[2]), pointer(*t[3]), (long long)nseq);
+    END_HANDLE_TH_ERRORS
+}
+
+// map_out(requests, max_blocks, rows, extra, device): a new state map's
+// cu_seqlens, seq_of, pos_of, slot_of, init_slot, table and free_head, then the
+// address of `extra` more int32: one allocation, each part on 16 bytes.
+PyObject* map_out(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (!arity("map_out", n, 5)) return nullptr;
+    int64_t v[4];
+    for (int i = 0; i < 4; ++i) {
+        v[i] = PyLong_AsLongLong(a[i]);
+        if (v[i] == -1 && PyErr_Occurred()) return nullptr;
+        if (v[i] < 0 || v[i] > std::numeric_limits<int>::max()) return PyErr_Format(PyExc_ValueError, "map_out: a size out of range");
+    }
+    if (!THPDevice_Check(a[4])) return PyErr_Format(PyExc_TypeError, "map_out: a device expected");
+    const int64_t reqs = v[0], blocks = v[1], T = v[2];
+    const auto on = at::TensorOptions().device(reinterpret_cast<THPDevice*>(a[4])->device);
+    const int64_t sizes[] = {reqs + 1, T, T, 2 * T, reqs, reqs * blocks, 1};   // in int32
+    int64_t at[8] = {0};
+    for (int i = 0; i < 7; ++i) at[i + 1] = at[i] + (sizes[i] + 3) / 4 * 4;
+    const at::Tensor whole = at::empty({at[7] + v[3]}, on.dtype(at::kInt));
+    auto view = [&](int i, at::IntArrayRef shape, at::IntArrayRef strides) {
+        // as detach() makes a second tensor of one storage, at a place and shape of its own
+        auto impl = whole.unsafeGetTensorImpl()->shallow_copy_and_detach(c10::VariableVersion(0), /*allow_tensor_metadata_change=*/true);
+        if (i == 3) impl->set_storage_and_dtype(whole.storage(), caffe2::TypeMeta::fromScalarType(at::kLong));
+        impl->set_sizes_and_strides(shape, strides, i == 3 ? at[i] / 2 : at[i]);
+        return THPVariable_Wrap(at::Tensor(std::move(impl)));
+    };
+    const int64_t row = blocks > 0 ? blocks : 1;
+    return Py_BuildValue("(NNNNNNNN)", view(0, {reqs + 1}, {1}), view(1, {T}, {1}), view(2, {T}, {1}), view(3, {T}, {1}),
+                         view(4, {reqs}, {1}), view(5, {reqs, blocks}, {row, 1}), view(6, {1}, {1}),
+                         PyLong_FromVoidPtr(whole.data_ptr<int>() + at[7]));
+    END_HANDLE_TH_ERRORS
+}
+
 // empty(shape, dtype, device): torch.empty
 PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -209,37 +300,6 @@ PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n)
     return THPVariable_Wrap(at::empty(at::IntArrayRef(dims, nd), at::TensorOptions()
                                                                      .dtype(reinterpret_cast<THPDtype*>(a[1])->scalar_type)
                                                                      .device(reinterpret_cast<THPDevice*>(a[2])->device)));
-    END_HANDLE_TH_ERRORS
-}
-
-// part(whole, shape, offset): a contiguous view of a 1-d tensor from an element on
-PyObject* part(PyObject*, PyObject* const* a, Py_ssize_t n)
-{
-    HANDLE_TH_ERRORS
-    if (!arity("part", n, 3)) return nullptr;
-    PyObject* name = PyUnicode_InternFromString("whole");
-    const at::Tensor* t = name ? as_tensor(a[0], name) : nullptr;
-    Py_XDECREF(name);
-    int64_t dims[kMaxDims], st[kMaxDims], count = 1;
-    bool empty = false;
-    const int nd = t ? as_dims(a[1], dims) : -1;
-    if (nd < 0) return nullptr;
-    const int64_t off = PyLong_AsLongLong(a[2]);
-    if (off == -1 && PyErr_Occurred()) return nullptr;
-    for (int i = nd - 1; i >= 0; --i) {
-        if (dims[i] < 0) return PyErr_Format(PyExc_ValueError, "part: a negative size");
-        st[i] = count;
-        empty |= dims[i] == 0;
-        count *= dims[i] > 0 ? dims[i] : 1;
-    }
-    if (t->dim() != 1 || !t->is_contiguous() || off < 0 || off + (empty ? 0 : count) > t->numel()) {
-        PyErr_SetString(PyExc_ValueError, "part: beyond the tensor");
-        return nullptr;
-    }
-    // as detach() makes a second tensor of one storage, at a place and shape of its own
-    auto impl = t->unsafeGetTensorImpl()->shallow_copy_and_detach(c10::VariableVersion(0), /*allow_tensor_metadata_change=*/true);
-    impl->set_sizes_and_strides(at::IntArrayRef(dims, nd), at::IntArrayRef(st, nd), t->storage_offset() + off);
-    return THPVariable_Wrap(at::Tensor(std::move(impl)));
     END_HANDLE_TH_ERRORS
 }
 
@@ -299,7 +359,9 @@ PyMethodDef methods[] = {
     {"rows", fast(rows), METH_FASTCALL, nullptr},
     {"bc", fast(bc), METH_FASTCALL, nullptr},
     {"empty", fast(empty), METH_FASTCALL, nullptr},
-    {"part", fast(part), METH_FASTCALL, nullptr},
+    {"where", fast(where), METH_FASTCALL, nullptr},
+    {"map_in", fast(map_in), METH_FASTCALL, nullptr},
+    {"map_out", fast(map_out), METH_FASTCALL, nullptr},
     ENTRY(ssd_state_map_workspace_bytes),
     ENTRY(ssd_state_map),
     ENTRY(ssd_conv1d_silu_varlen),

@@ -67,14 +67,14 @@ class _On:
             raise ValueError("CUDA tensors expected")
         if _native is None:
             _load()
-        self.device = like.device
-        index = like.get_device()
-        if stream is not None and stream.device != self.device:
-            raise ValueError("stream and tensors are on different devices")
-        self.switch = None if index == torch.cuda.current_device() else torch.cuda.device(self.device)
-        now = torch._C._cuda_getCurrentRawStream(index)
-        self.handle = now if stream is None else stream.cuda_stream
-        self.other = stream if self.handle != now else None
+        self.device, self.handle, current = _native.where(like)
+        self.switch = None if current else torch.cuda.device(self.device)
+        self.other = None
+        if stream is not None:
+            if stream.device != self.device:
+                raise ValueError("stream and tensors are on different devices")
+            if stream.cuda_stream != self.handle:
+                self.handle, self.other = stream.cuda_stream, stream
 
     def __enter__(self):
         if self.switch is not None:
@@ -94,6 +94,16 @@ class _On:
         t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
+    def map_out(self, n, max_blocks, T, extra):
+        """A new map's tensors, and the address of `extra` more int32."""
+        if self.other is None:
+            return _native.map_out(n, max_blocks, T, extra, self.device)
+        with torch.cuda.stream(self.other):
+            made = _native.map_out(n, max_blocks, T, extra, self.device)
+        for t in made[:-1]:
+            t.record_stream(torch.cuda.current_stream(self.device))
+        return made
+
     def workspace(self, given, need: int):
         """(pointer, bytes) of the caller's workspace, or of a new one."""
         if given is None:
@@ -107,9 +117,7 @@ class _On:
 
 def _map(m: StateMap, T: int, device):
     """The pointers of a StateMap, its requests and block size."""
-    n = m.cu_seqlens.numel() - 1
-    return (_dense(m.cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), device), _dense(m.seq_of, "seq_of", torch.int32, (T,), device),
-            _dense(m.slot_of, "slot_of", torch.int64, (T,), device), _dense(m.init_slot, "init_slot", torch.int32, (n,), device), n)
+    return _native.map_in(m[0], m[1], m[3], m[4], T, device)
 
 
 def _status(status, on):
@@ -140,19 +148,11 @@ def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_l
         dev = on.device
         scratch = 64 + n      # the workspace, in int32
         if out is None:
-            # one allocation for the int32 parts (seq_of and pos_of on 16
-            # bytes) and the workspace
-            n4, T4 = (n + 4) // 4 * 4, (T + 3) // 4 * 4
-            at_pos, at_init, at_table = n4 + T4, n4 + 2 * T4, 2 * n4 + 2 * T4
-            at_head = at_table + n * mb
-            parts = on.empty((at_head + 1 + (0 if workspace is not None else scratch),), i32)
-            part = _native.part
-            out = StateMap(part(parts, (n + 1,), 0), part(parts, (T,), n4), part(parts, (T,), at_pos), on.empty((T,), torch.int64),
-                           part(parts, (n,), at_init), part(parts, (n, mb), at_table), part(parts, (1,), at_head), block_tokens)
-            at = parts.data_ptr()
-            ptrs = (at, at + 4 * n4, at + 4 * at_pos, out.slot_of.data_ptr(), at + 4 * at_init, at + 4 * at_table, at + 4 * at_head)
+            *parts, end = on.map_out(n, mb, T, 0 if workspace is not None else scratch)
+            out = StateMap(*parts, block_tokens)
+            ptrs = [t.data_ptr() for t in parts]
             if workspace is None:
-                wp, wb = ptrs[-1] + 4, 4 * scratch
+                wp, wb = end, 4 * scratch
         else:
             cu, seq, slot, init, _ = _map(out, T, dev)
             ptrs = (cu, seq, _dense(out.pos_of, "pos_of", i32, (T,), dev), slot, init, _dense(out.table, "out.table", i32, (n, mb), dev),

@@ -82,18 +82,51 @@ def test_bc(ext):
         ext.bc(B, None, (2, 5), p)
 
 
-def test_empty_and_part(ext):
+def test_empty(ext):
     e = ext.empty((3, 0, 2), BF16, CPU)
     assert e.shape == (3, 0, 2) and e.dtype == BF16
-    whole = torch.arange(20, dtype=torch.int32)
-    p = ext.part(whole, (2, 3), 5)
-    assert p.tolist() == [[5, 6, 7], [8, 9, 10]] and p.is_contiguous() and p.untyped_storage().data_ptr() == whole.data_ptr()
-    p[0, 0] = -1
-    assert whole[5] == -1
-    assert ext.part(whole, (4, 0), 20).shape == (4, 0) and ext.part(whole, (20,), 0).numel() == 20
-    for shape, off in (((21,), 0), ((1,), 20), ((3, 3), 12), ((1,), -1), ((-1,), 0)):
+
+
+@pytest.mark.parametrize("n,blocks,T", [(3, 2, 7), (0, 0, 0), (1, 0, 5), (5, 4, 0), (9, 3, 16)])
+def test_map_out(ext, n, blocks, T):
+    *parts, end = ext.map_out(n, blocks, T, 11, CPU)
+    shapes = [(n + 1,), (T,), (T,), (T,), (n,), (n, blocks), (1,)]
+    assert [tuple(p.shape) for p in parts] == shapes and all(p.is_contiguous() for p in parts)
+    assert [p.dtype for p in parts] == [torch.int32] * 3 + [torch.int64] + [torch.int32] * 3
+    # no part overlaps another, the last 11 entries neither; each on 16 bytes
+    whole = parts[0].untyped_storage()
+    assert end + 44 == whole.data_ptr() + whole.nbytes()
+    spans = sorted((p.data_ptr(), p.data_ptr() + p.element_size() * p.numel()) for p in parts if p.numel())
+    assert all(hi <= lo for (_, hi), (lo, _) in zip(spans, spans[1:] + [(end, 0)]))
+    assert all((p.data_ptr() - whole.data_ptr()) % 16 == 0 for p in parts if p.numel())
+    for i, p in enumerate(parts):
+        p.fill_(i)
+    assert all((p == i).all() for i, p in enumerate(parts))
+    with pytest.raises(ValueError):
+        ext.map_out(-1, blocks, T, 0, CPU)
+    with pytest.raises(ValueError):
+        ext.map_out(n, blocks, 2 ** 31, 0, CPU)
+
+
+def test_map_in(ext):
+    i32, i64 = torch.int32, torch.int64
+    m = [torch.zeros(4, dtype=i32), torch.zeros(7, dtype=i32), torch.zeros(7, dtype=i64), torch.zeros(3, dtype=i32)]
+    assert ext.map_in(*m, 7, CPU) == (*(t.data_ptr() for t in m), 3)
+    for i, bad in ((1, torch.zeros(6, dtype=i32)), (2, torch.zeros(7, dtype=i32)), (3, torch.zeros(4, dtype=i32)), (0, torch.zeros(0, dtype=i32)),
+                   (0, torch.zeros(2, 2, dtype=i32)), (1, torch.zeros(14, dtype=i32)[::2])):
         with pytest.raises(ValueError):
-            ext.part(whole, shape, off)
+            ext.map_in(*m[:i], bad, *m[i + 1:], 7, CPU)
+    with pytest.raises(ValueError, match=r"seq_of must be a contiguous torch.int32 tensor of shape \(8,\) on cpu"):
+        ext.map_in(*m, 8, CPU)
+    with pytest.raises(TypeError, match="init_slot must be a tensor"):
+        ext.map_in(*m[:3], None, 7, CPU)
+
+
+def test_where_wants_a_cuda_tensor(ext):
+    with pytest.raises(ValueError, match="CUDA tensors expected"):
+        ext.where(torch.zeros(3))
+    with pytest.raises(TypeError):
+        ext.where(3)
 
 
 def test_arguments(ext):
