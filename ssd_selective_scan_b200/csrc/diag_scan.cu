@@ -609,12 +609,13 @@ cudaError_t launch_diag_ckpt(const DiagArgs& a, cudaStream_t s)
     return a.bf16 ? launch_t<__nv_bfloat16, false, kCkpt>(a, seg, s) : launch_t<float, false, kCkpt>(a, seg, s);
 }
 
-// Rows per piece of the walk that keeps states: as the forward scan's, in
-// whole backward pieces.
+// Rows per piece of the walk that keeps states: as the forward scan's, to the
+// nearest whole number of backward pieces.
 int diag_ckpt_rows(int b, int L, int E, int N, int G, int bseg)
 {
     const int64_t seg = piece_rows(b, b * L, E, N, G);
-    const int64_t whole = (seg + bseg - 1) / bseg * bseg;
+    const int64_t near = (seg + bseg / 2) / bseg * bseg;
+    const int64_t whole = near > bseg ? near : bseg;
     return seg < L && whole < L ? (int)whole : L;
 }
 

@@ -42,8 +42,8 @@
 // formed once per token and channel) while the other finishes du, ddt_raw and
 // dz of the last one from its sums, in 16-byte vectors.
 //
-// 8 x 2048 tokens of 2560 gated bf16 channels, 16 states: 990 us, the forward
-// walk 468, the sums 15.  Bound by instruction issue (27 per token, channel
+// 8 x 2048 tokens of 2560 gated bf16 channels, 16 states: 1440 us for the call,
+// about 960 of them here, the forward walk 468, the sums 15.  Bound by instruction issue (27 per token, channel
 // and state, 53% of the issue slots: 168 registers hold the 4 rows, so 12
 // warps share an SM) and by shared memory's wavefronts (54%), not by HBM.
 #include "diag_tile.cuh"
@@ -543,21 +543,28 @@ __global__ void __launch_bounds__(kSumThreads) diag_sum_kernel(const SumArgs a)
 
 // Rows per piece.  The forward walk pays for the pieces (306 us without, 468
 // with them, at 8 x 2048 rows of 2560 channels), this kernel gains from them
-// (1390 us whole, 2 or 3 CTAs on an SM for all of its time; 990 cut), so rows
-// are cut where whole sequences make less than kLeastPerSm CTAs an SM, which
-// holds 3 at a time, and then until there are kCutPerSm (9 and 24 are within
-// 1.5%).
+// (1390 us whole, 2 or 3 CTAs on an SM for all of its time), so rows are cut
+// where whole sequences make less than kLeastPerSm CTAs an SM.  An SM holds
+// kPerSm at a time; the pieces are the longest that take the device up 2.5
+// times or more, else the shortest, and where those take it up less than 1.25
+// times, such as fit it at once (a few CTAs of a second round would take as long
+// as the first).  The whole call, 8 x 2048 x 2560: 512 rows (2.9 times) 1441 us,
+// 192 1452, 320 1473, 96 1517, 64 1576; 4 x 2048 x 2560: 384 rows 898, 256 940,
+// 160 962, 512 (1.4 times) 1000; 8 x 256 x 2048: 64 rows (2.3 times) 185, 96 210; 1 x
+// 2048 x 1024: 64 rows (1.15 times) 141, 96 120, 192 162; 2 x 517 x 784: 64
+// rows (0.95 times) 89, 96 112.
 constexpr int kLeastPerSm = 12;
-constexpr int kCutPerSm = 15;
-constexpr int kPieceLeast = 64;
+constexpr int kPerSm = 3;
+constexpr int kPieceMost = 512, kPieceLeast = 64;
 
 int bwd_piece_rows(int b, int L, int E, int N, int G)
 {
     const int64_t ctas = (int64_t)b * channel_tiles(E, G, kWarps * 64 / tile_lanes(N)) * G;
+    const int64_t at_once = (int64_t)sm_count() * kPerSm;
     if (ctas >= (int64_t)sm_count() * kLeastPerSm) return L;
-    const int64_t pieces = ((int64_t)sm_count() * kCutPerSm + ctas - 1) / ctas;
-    int64_t seg = ((int64_t)L + pieces - 1) / pieces;
-    seg = (seg + 31) / 32 * 32;
+    int64_t seg = kPieceMost;
+    while (seg > kPieceLeast && (seg >= L || 2 * ctas * L < 5 * at_once * seg)) seg /= 2;
+    if (4 * ctas * L < 5 * at_once * seg) seg = (ctas * L + at_once * 32 - 1) / (at_once * 32) * 32;
     if (seg < kPieceLeast) seg = kPieceLeast;
     return seg < L ? (int)seg : L;
 }
