@@ -3,9 +3,9 @@
 libssd.so (built from csrc/ by ``python -m ssd_selective_scan_b200.build``)
 holds the CUDA kernels behind the C ABI of include/ssd.h and
 include/ssd_diag.h; ``binding`` is its ctypes binding, ``layer`` the
-torch-facing calls and ``diag`` those of the diagonal selective scan.  The library is loaded
-on first use and there is no fallback path: without libssd.so every call
-raises.
+torch-facing calls and ``diag`` those of the diagonal selective scan, which go
+through the extension _pycall.so (csrc/pycall.cpp).  Both are loaded on first
+use and there is no fallback path: without them every call raises.
 """
 from .layer import (chunk_scan_bwd, chunk_scan_bwd_workspace_bytes, chunk_scan_fwd, chunk_scan_fwd_varlen, chunk_scan_varlen_workspace_bytes,
                     chunk_scan_workspace_bytes, conv1d_silu, conv_scan_fwd, conv_scan_workspace_bytes,
