@@ -105,3 +105,59 @@ def test_state_map_reads_the_last_state_only():
     m = fwd.call_map(q, T, st)
     fwd.assert_map(m, R.ref_map(q, T))
     assert st.item() == 0
+
+
+def _serve(q, E, N, k, states, cache, dtype):
+    """A step of prompts and one of single tokens over these pools; (y, the
+    slots that hold each request's last state)."""
+    g = torch.Generator().manual_seed(12)
+    st = fwd.zero_status()
+    n = len(q["lens"])
+    w, ctx, ys = (0.5 * torch.randn(E, k, generator=g)).cuda(), fwd.up(q["ctx"]), []
+    table, free, head = fwd.up(q["table"]), fwd.up(q["free"]), fwd.up([q["head"]])
+    for lens in (q["lens"], [1] * n):
+        T = int(sum(lens))
+        p = fwd.cuda(R.scan_inputs((T,), E, N, 1, dtype, seed=T))
+        m = ssd.state_map(fwd.up(lens), ctx, table, free, head, T, q["bs"], q["nslots"], status=st)
+        p["u"] = ssd.conv1d_silu_varlen(p["u"], w, cache, m, status=st)
+        call = ssd.diag_scan_fwd_varlen if T > n else None
+        ys.append(call(**p, states=states, m=m, status=st) if call else
+                  ssd.diag_state_update(states, p["u"], p["dt_raw"], p["A"], p["B"], p["C"], m, dt_bias=p["dt_bias"], D=p["D"], z=p["z"], status=st))
+        table, head, ctx = m.table, m.free_head, ctx + fwd.up(lens)
+    assert st.item() == 0
+    last = table.gather(1, ((ctx.long() - 1) // q["bs"])[:, None])[:, 0]
+    return torch.cat(ys), last
+
+
+@pytest.mark.parametrize("bs,pool", [(1 << 28, None), (8, 17000), (1 << 18, 17000)], ids=["long_blocks", "large_pool", "both"])
+def test_offsets_beyond_32_bits(bs, pool):
+    """Places of tokens (slot * block_tokens) and of states (slot * E * N) past
+    2^32: what a small pool of short blocks' slots gives."""
+    E, N, k = 8192, 16, 4
+    lens, ctx = [20, 1, 7], [0, 30, 8]
+
+    def run(bs, pool):
+        q = R.batch(lens, ctx, bs, seed=2, spare=40)
+        if pool is not None:     # the slots at the pool's far end
+            far = pool - q["nslots"]
+            held = q["table"] >= 0
+            q["table"][held] += far
+            q["free"] = q["free"] + far
+            q["nslots"] = pool
+        states = torch.empty(q["nslots"], E, N, device="cuda")
+        cache = torch.empty(q["nslots"], E, k, dtype=BF16, device="cuda")
+        g = torch.Generator().manual_seed(5)
+        for r in range(3):
+            if ctx[r]:
+                slot = q["table"][r, (ctx[r] - 1) // bs]
+                states[slot] = torch.randn(E, N, generator=g).cuda()
+                cache[slot] = torch.randn(E, k, generator=g).to(BF16).cuda()
+        y, last = _serve(q, E, N, k, states, cache, BF16)
+        if bs > 1 << 16 or pool:
+            assert int(last.max()) * max(bs, E * N) > 1 << (31 if pool else 32)
+        return y, states[last], cache[last]
+
+    want, got = run(8, None), run(bs, pool)
+    assert torch.equal(got[2], want[2]), "caches"
+    for a, b, what in zip(got, want, ("y", "states")):
+        R.close(a, b.double(), what)
