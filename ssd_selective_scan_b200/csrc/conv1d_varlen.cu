@@ -169,18 +169,30 @@ conv1d_varlen_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
     walk_piece<T, K, kGroup>(p, x, xs, out, os, taps, cache, sl, E, c0);
 }
 
+// A piece among single tokens.  Out of line, with taps of its own, so that its
+// registers are not every CTA's.
+template <typename T, int K>
+__device__ __noinline__ void walk_rare(int q, const T* x, int64_t xs, T* out, int64_t os, const float* w, const float* bias, T* cache,
+                                       const Slots* slots, int rows, int E, int c0)
+{
+    const Slots sl = *slots;
+    Piece p;
+    if (!find_piece_packed(q, sl, rows, kPiece, K - 2, p)) return;
+    Taps<K> taps;
+    taps.load(w, bias, c0);
+    walk_piece<T, K, kGroupFew>(p, x, xs, out, os, taps, cache, sl, E, c0);
+}
+
 // Batches of single tokens: a CTA takes SEQS sequences of its channels, so
 // that their taps (64 bytes a thread, against 8 of x) are read once for all
 // and their caches are on the way together.  Sequences of more tokens (a
 // prompt among the single tokens) are walked in pieces: the first by the CTA
 // that has the sequence, those behind by the CTAs in turn, one to each at most,
 // as there are at most two rows to a sequence.
-// (The CTAs an SM must hold are set by what single tokens need; the walk of a
-// long sequence spills 20 registers for it.)
 template <typename T, int K, int SEQS>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4)
 conv1d_tokens_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, int64_t os, const float* __restrict__ w,
-                     const float* __restrict__ bias, T* cache, const Slots sl, int rows, int E)
+                     const float* __restrict__ bias, T* cache, const __grid_constant__ Slots sl, int rows, int E)
 {
     static_assert(2 * SEQS <= kPiece, "a CTA has one later piece at most");
     __shared__ int first[SEQS], count[SEQS], init[SEQS], slot[SEQS], later;
@@ -243,9 +255,7 @@ conv1d_tokens_kernel(const T* __restrict__ x, int64_t xs, T* __restrict__ out, i
 #pragma unroll 1
     for (int i = 0; i <= SEQS; ++i) {
         if (i < SEQS ? count[i] <= 1 : !later) continue;
-        Piece p;
-        if (find_piece_packed(i < SEQS ? (int)blockIdx.x * SEQS + i : sl.nseq + (int)blockIdx.x, sl, rows, kPiece, K - 2, p))
-            walk_piece<T, K, kGroupFew>(p, x, xs, out, os, taps, cache, sl, E, c0);
+        walk_rare<T, K>(i < SEQS ? (int)blockIdx.x * SEQS + i : sl.nseq + (int)blockIdx.x, x, xs, out, os, w, bias, cache, &sl, rows, E, c0);
     }
 }
 
@@ -258,8 +268,9 @@ cudaError_t launch_k(const void* x, int64_t xs, void* out, int64_t os, const flo
     const unsigned cols = (unsigned)((E + per - 1) / per);
     if (rows <= 2 * (int64_t)a.nseq) {
         // 256 tokens of 8192 bf16 channels 14.7 us (2.9 TB/s), 512 24.8, 256 of 2560
-        // 5.1, 16 of 4096 3.6; 4 sequences to a CTA, 4 CTAs an SM: 14.7, 26.3, 5.5,
-        // 4.4; 8 and 3: 20.2, 30.6, 7.7, 6.7.  256 tokens of 8192 f32 channels 24.3.
+        // 5.3, 16 of 4096 3.3; 4 sequences to a CTA, 4 CTAs an SM: 14.7, 26.3, 5.5,
+        // 4.4; 8 and 3: 20.2, 30.6, 7.7, 6.7; 2 and 8 CTAs (spills) 15.2, 25.6, 5.7,
+        // 3.7.  256 tokens of 8192 f32 channels 20.9 (24.3 with the rare walk in line).
         constexpr int SEQS = 2;
         conv1d_tokens_kernel<T, K, SEQS><<<dim3((unsigned)((a.nseq + SEQS - 1) / SEQS), cols), kThreads, 0, s>>>(
             static_cast<const T*>(x), xs, static_cast<T*>(out), os, w, bias, static_cast<T*>(cache), sl, rows, E);
