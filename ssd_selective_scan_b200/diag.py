@@ -134,7 +134,8 @@ def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_l
     tokens), table [n, max_blocks] int32 (slots of the held blocks), free_list
     [nfree] and free_head [1] int32; T rows in the packed batch.  Returns a
     StateMap whose table and free_head are the updated ones (new tensors, or
-    `out`'s, which may be the inputs for an update in place).  A batch that
+    `out`'s, which may be the inputs for an update in place; `out` is for n
+    requests, T rows and this block size).  A batch that
     does not fit (ssd_diag.h) leaves SSD_ERR_INVALID_ARG in `status` and gives
     an empty map."""
     n = lens.numel()
@@ -154,7 +155,9 @@ def state_map(lens: torch.Tensor, ctx: torch.Tensor, table: torch.Tensor, free_l
             if workspace is None:
                 wp, wb = end, 4 * scratch
         else:
-            cu, seq, slot, init, _ = _map(out, T, dev)
+            cu, seq, slot, init, made_for = _map(out, T, dev)
+            if made_for != n:   # its tensors would be written past their ends, or keep old requests
+                raise ValueError(f"out is the map of {made_for} requests, lens of {n}")
             ptrs = (cu, seq, _dense(out.pos_of, "pos_of", i32, (T,), dev), slot, init, _dense(out.table, "out.table", i32, (n, mb), dev),
                     _dense(out.free_head, "out.free_head", i32, (1,), dev))
             if workspace is None:
