@@ -35,8 +35,9 @@ _native = _dense = _rows = _bc = None
 
 def _load():
     global _native, _dense, _rows, _bc
-    _native = libssd.load_pycall()
-    _dense, _rows, _bc = _native.dense, _native.rows, _native.bc
+    ext = libssd.load_pycall()
+    _dense, _rows, _bc = ext.dense, ext.rows, ext.bc
+    _native = ext     # last: it tells another thread that the checks are there
 
 
 class StateMap(NamedTuple):

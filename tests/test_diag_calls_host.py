@@ -70,3 +70,22 @@ def test_state_map_out_of_other_rows(calls):
     with pytest.raises(ValueError, match="another block size"):
         diag.state_map(**requests(3), T=7, block_tokens=8, nslots=9, out=old)
     assert len(calls) == 1 and isinstance(old, StateMap)
+
+
+def test_first_use_from_two_threads(ext, monkeypatch):
+    """Another thread takes the extension for loaded when it sees `_native`:
+    the checks that it then calls have to be there."""
+    seen = []
+
+    class Slow:
+        def __getattr__(self, name):
+            seen.append((name, diag._native))     # what another thread would find now
+            return getattr(ext, name)
+
+    for name in ("_native", "_dense", "_rows", "_bc"):
+        monkeypatch.setattr(diag, name, None)
+    monkeypatch.setattr(libssd, "load_pycall", Slow)
+    diag._load()
+    assert {n for n, _ in seen} == {"dense", "rows", "bc"}
+    assert all(native is None for _, native in seen)
+    assert diag._native is not None and None not in (diag._dense, diag._rows, diag._bc)
