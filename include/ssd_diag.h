@@ -158,11 +158,13 @@ SSD_API ssd_status_t ssd_conv1d_silu_bwd(const void* x, const float* w, const fl
  *   init_state [b][E][N] float32, may be NULL (zero)
  *   y      [b][L][E] dtype, written; must not overlap inputs
  *   final_state [b][E][N] float32, may be NULL; may be init_state
- *   workspace  ssd_diag_scan_workspace_bytes(b, b*L, E, N, G) bytes (0 for
- *              batches that fill the device by themselves), no initial contents
+ *   workspace  ssd_diag_scan_fwd_workspace_bytes(b, L, E, N, G) bytes, no
+ *              initial contents: 0 where no sequence is cut (batches that fill
+ *              the device by themselves, sequences no longer than a piece).
+ *              ssd_diag_scan_workspace_bytes(b, b*L, E, N, G) is never less
  * L == 0 copies init_state (or zeros) into final_state.
  */
-SSD_API size_t ssd_diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G);
+SSD_API size_t ssd_diag_scan_fwd_workspace_bytes(int b, int L, int E, int N, int G);
 SSD_API ssd_status_t ssd_diag_scan_fwd(const void* u, int64_t u_stride, const void* dt_raw, int64_t dt_stride,
                                        const void* z, int64_t z_stride, const void* B, const void* C,
                                        int64_t bc_stride, const float* A, const float* dt_bias, const float* D,
@@ -175,9 +177,12 @@ SSD_API ssd_status_t ssd_diag_scan_fwd(const void* u, int64_t u_stride, const vo
  *
  *   u, dt_raw, z, B, C as above with T rows; y [T][E] dtype
  *   states [nslots][E][N] float32, read and written by slot
- *   workspace  ssd_diag_scan_workspace_bytes(nseq, T, E, N, G) bytes
+ *   workspace  ssd_diag_scan_workspace_bytes(nseq, T, E, N, G) bytes (0 for
+ *              batches that fill the device by themselves): for any lengths
+ *              that the map may hold
  *   status REQUIRED
  */
+SSD_API size_t ssd_diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G);
 SSD_API ssd_status_t ssd_diag_scan_fwd_varlen(const void* u, int64_t u_stride, const void* dt_raw,
                                               int64_t dt_stride, const void* z, int64_t z_stride, const void* B,
                                               const void* C, int64_t bc_stride, const float* A,

@@ -69,6 +69,7 @@ DIAG_SIGNATURES = {
     "ssd_conv1d_silu_bwd_workspace_bytes": (_sz, [_i] * 4),
     "ssd_conv1d_silu_bwd": (_i, [_vp] * 9 + [_i] * 5 + [_vp, _sz, _vp]),
     "ssd_diag_scan_workspace_bytes": (_sz, [_i] * 5),
+    "ssd_diag_scan_fwd_workspace_bytes": (_sz, [_i] * 5),
     "ssd_diag_scan_fwd": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 6 + [_i] * 6 + [_vp, _sz, _vp]),
     "ssd_diag_scan_fwd_varlen": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64] + [_vp] * 9 + [_i] * 8 +
                                  [_vp, _sz, _vp, _vp]),
@@ -259,6 +260,10 @@ def ssd_conv1d_silu_bwd(x, w, bias, conv_state, dout, dx, dw, dbias, dconv_state
 
 def ssd_diag_scan_workspace_bytes(nseq, rows, E, N, G) -> int:
     return load().ssd_diag_scan_workspace_bytes(nseq, rows, E, N, G)
+
+
+def ssd_diag_scan_fwd_workspace_bytes(b, L, E, N, G) -> int:
+    return load().ssd_diag_scan_fwd_workspace_bytes(b, L, E, N, G)
 
 
 def ssd_diag_scan_fwd(u, u_stride, dt_raw, dt_stride, z, z_stride, B, C, bc_stride, A, dt_bias, D, init_state, y,

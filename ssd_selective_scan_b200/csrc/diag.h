@@ -65,7 +65,9 @@ inline bool bc_aligned(const DiagArgs& a, size_t elem)
 {
     return a.bcs % 4 == 0 && reinterpret_cast<uintptr_t>(a.B) % (4 * elem) == 0 && reinterpret_cast<uintptr_t>(a.C) % (4 * elem) == 0;
 }
+// Of packed sequences, whatever their lengths; and of dense ones.
 size_t diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G);
+size_t diag_scan_fwd_workspace_bytes(int b, int L, int E, int N, int G);
 cudaError_t launch_diag_scan(const DiagArgs& a, cudaStream_t s);
 cudaError_t launch_diag_update(const DiagArgs& a, cudaStream_t s);
 

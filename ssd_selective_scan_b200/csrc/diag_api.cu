@@ -194,6 +194,12 @@ size_t ssd_diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G)
     return diag_scan_workspace_bytes(nseq, rows, E, N, G);
 }
 
+size_t ssd_diag_scan_fwd_workspace_bytes(int b, int L, int E, int N, int G)
+{
+    if (b <= 0 || L <= 0 || (int64_t)b * L > kMaxRows || E <= 0 || N <= 0 || N > 64 || G <= 0 || E % G) return 0;
+    return diag_scan_fwd_workspace_bytes(b, L, E, N, G);
+}
+
 ssd_status_t ssd_diag_scan_fwd(const void* u, int64_t u_stride, const void* dt_raw, int64_t dt_stride, const void* z,
                                int64_t z_stride, const void* B, const void* C, int64_t bc_stride, const float* A,
                                const float* dt_bias, const float* D, const float* init_state, void* y,
@@ -207,7 +213,7 @@ ssd_status_t ssd_diag_scan_fwd(const void* u, int64_t u_stride, const void* dt_r
     const ssd_status_t st = check_scan(a, dtype);
     if (st != SSD_OK) return st;
     if (a.rows > 0 && !y) return SSD_ERR_INVALID_ARG;
-    const size_t need = ssd_diag_scan_workspace_bytes(b, a.rows, E, N, G);
+    const size_t need = ssd_diag_scan_fwd_workspace_bytes(b, L, E, N, G);
     if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return SSD_ERR_INVALID_ARG;
     const ScanRanges r = scan_ranges(a, elem_bytes(dtype));
     const int64_t st_bytes = (int64_t)b * E * N * 4;

@@ -529,7 +529,7 @@ constexpr int kPieceLeast = 128;        // rows; a shorter piece costs more to j
 // Rows per piece, or no cut (the rows' count): one sequence that had all the
 // rows would get as many pieces as fill the device; sequences shorter than a
 // piece stay whole (packed ones are cut into pieces of up to twice that).
-int piece_rows(int nseq, int rows, int E, int N, int G)
+int piece_rows(int rows, int E, int N, int G)
 {
     const int ch = kWarps * 64 / tile_lanes(N);
     const int64_t pieces = kWarpsWanted / ((int64_t)channel_tiles(E, G, ch) * G * kWarps);
@@ -589,15 +589,21 @@ cudaError_t launch_t(const DiagArgs& args, int seg, cudaStream_t s)
 
 size_t diag_scan_workspace_bytes(int nseq, int rows, int E, int N, int G)
 {
-    const int seg = piece_rows(nseq, rows, E, N, G);
+    const int seg = piece_rows(rows, E, N, G);
     if (seg >= rows) return 0;
     // packed or dense: a dense batch has at most one short piece per sequence
     return cut_ws_bytes(nseq, nseq + ((int64_t)rows - 1) / seg + 1, E, N);
 }
 
+// (sequences no longer than a piece are launched whole: launch_lpc)
+size_t diag_scan_fwd_workspace_bytes(int b, int L, int E, int N, int G)
+{
+    return piece_rows(b * L, E, N, G) < L ? diag_scan_workspace_bytes(b, b * L, E, N, G) : 0;
+}
+
 cudaError_t launch_diag_scan(const DiagArgs& a, cudaStream_t s)
 {
-    const int seg = piece_rows(a.nseq, a.rows, a.E, a.N, a.G);
+    const int seg = piece_rows(a.rows, a.E, a.N, a.G);
     if (a.sl.cu) return a.bf16 ? launch_t<__nv_bfloat16, true, kOutput>(a, seg, s) : launch_t<float, true, kOutput>(a, seg, s);
     return a.bf16 ? launch_t<__nv_bfloat16, false, kOutput>(a, seg, s) : launch_t<float, false, kOutput>(a, seg, s);
 }
@@ -613,7 +619,7 @@ cudaError_t launch_diag_ckpt(const DiagArgs& a, cudaStream_t s)
 // nearest whole number of backward pieces.
 int diag_ckpt_rows(int b, int L, int E, int N, int G, int bseg)
 {
-    const int64_t seg = piece_rows(b, b * L, E, N, G);
+    const int64_t seg = piece_rows(b * L, E, N, G);
     const int64_t near = (seg + bseg / 2) / bseg * bseg;
     const int64_t whole = near > bseg ? near : bseg;
     return seg < L && whole < L ? (int)whole : L;

@@ -368,6 +368,7 @@ PyMethodDef methods[] = {
     ENTRY(ssd_conv1d_silu_bwd_workspace_bytes),
     ENTRY(ssd_conv1d_silu_bwd),
     ENTRY(ssd_diag_scan_workspace_bytes),
+    ENTRY(ssd_diag_scan_fwd_workspace_bytes),
     ENTRY(ssd_diag_scan_fwd),
     ENTRY(ssd_diag_scan_fwd_varlen),
     ENTRY(ssd_diag_scan_bwd_workspace_bytes),

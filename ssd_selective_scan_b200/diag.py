@@ -225,8 +225,9 @@ def conv1d_silu_bwd(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, bias: 
 
 
 def diag_scan_workspace_bytes(nseq: int, rows: int, E: int, N: int, G: int) -> int:
-    """Workspace of diag_scan_fwd (nseq = b, rows = b * L) and of
-    diag_scan_fwd_varlen (rows = T)."""
+    """Workspace of diag_scan_fwd_varlen (rows = T), and enough for
+    diag_scan_fwd (nseq = b, rows = b * L; none where its sequences are not
+    cut: ssd_diag.h)."""
     return int(libssd.ssd_diag_scan_workspace_bytes(nseq, rows, E, N, G))
 
 
@@ -254,7 +255,7 @@ def diag_scan_fwd(u: torch.Tensor, dt_raw: torch.Tensor, A: torch.Tensor, B: tor
         up, us = _rows(u, "u", (b, L), E, u)
         dp, ds = _rows(dt_raw, "dt_raw", (b, L), E, u)
         zp, zs = _rows(z, "z", (b, L), E, u)
-        wp, wb = on.workspace(workspace, _native.ssd_diag_scan_workspace_bytes(b, b * L, E, N, G))
+        wp, wb = on.workspace(workspace, _native.ssd_diag_scan_fwd_workspace_bytes(b, L, E, N, G))
         st = _native.ssd_diag_scan_fwd(up, us, dp, ds, zp, zs, pB, pC, bcs, _dense(A, "A", f32, (E, N), dev),
                                        _dense(dt_bias, "dt_bias", f32, (E,), dev), _dense(D, "D", f32, (E,), dev),
                                        _dense(init_state, "init_state", f32, (b, E, N), dev), _dense(y, "y", u.dtype, (b, L, E), dev),

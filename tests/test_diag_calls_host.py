@@ -89,3 +89,27 @@ def test_first_use_from_two_threads(ext, monkeypatch):
     assert {n for n, _ in seen} == {"dense", "rows", "bc"}
     assert all(native is None for _, native in seen)
     assert diag._native is not None and None not in (diag._dense, diag._rows, diag._bc)
+
+
+def dense(b, L, E, N=16, G=1):
+    f = lambda *s: torch.zeros(*s)  # noqa: E731
+    return dict(u=f(b, L, E), dt_raw=f(b, L, E), A=f(E, N), B=f(b, L, G, N), C=f(b, L, G, N))
+
+
+@pytest.mark.parametrize("b,L,E,cut", [(16384, 1, 128, False), (512, 100, 64, False), (40, 128, 64, False), (40, 129, 64, True), (1, 4096, 64, True),
+                                       (1, 100, 64, False), (64, 300, 8192, False)])
+def test_dense_scan_asks_for_what_it_uses(calls, b, L, E, cut):
+    """Sequences no longer than a piece are not cut, however many they are:
+    the call takes no workspace for them."""
+    need = libssd.ssd_diag_scan_fwd_workspace_bytes(b, L, E, 16, 1)
+    assert (need > 0) == cut
+    assert need == (libssd.ssd_diag_scan_workspace_bytes(b, b * L, E, 16, 1) if cut else 0)
+    if b * L * E < 1 << 23:
+        diag.diag_scan_fwd(**dense(b, L, E))
+        (name, a), = calls
+        assert name == "ssd_diag_scan_fwd" and a[-2] == need and (a[-3] is None) == (need == 0)
+
+
+def test_dense_scan_workspace_of_no_call():
+    for bad in ((0, 5, 64, 16, 1), (1, 0, 64, 16, 1), (1, 5, 64, 80, 1), (1, 5, 64, 16, 0), (1 << 16, 1 << 16, 64, 16, 1)):
+        assert libssd.ssd_diag_scan_fwd_workspace_bytes(*bad) == 0
