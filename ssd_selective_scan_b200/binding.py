@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 import threading
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -108,13 +109,25 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+def pycall_target() -> str:
+    """The torch and Python whose headers the extension is built against: it
+    reads tensors by their layout there."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def load_pycall():
-    """The extension module of csrc/pycall.cpp.  Raises if it has not been built."""
+    """The extension module of csrc/pycall.cpp.  Raises if it has not been
+    built, or for another torch or Python."""
     load()
     try:
         from . import _pycall
     except ImportError as e:
         raise RuntimeError(f"{PYCALL_PATH}: {e}; build it with `python -m ssd_selective_scan_b200.build` (there is no fallback path)") from e
+    built_for = getattr(_pycall, "built_for", "an unknown torch")
+    if built_for != pycall_target():
+        raise RuntimeError(f"{PYCALL_PATH} is built for {built_for}, this is {pycall_target()}: "
+                           "build it with `python -m ssd_selective_scan_b200.build`")
     return _pycall
 
 

@@ -6,7 +6,8 @@ extension _pycall.so from csrc/pycall.cpp.
 Each translation unit is compiled by nvcc into _build/ (in parallel), then
 linked into ssd_selective_scan_b200/libssd.so with the static CUDA runtime.
 Only sm_100a SASS is generated: the library targets B200 alone.  The extension
-is host code against torch's and Python's headers, linked to libssd.so beside it.
+is host code against torch's and Python's headers, linked to libssd.so beside
+it; it is built anew when either of the two is another version.
 """
 from __future__ import annotations
 
@@ -19,6 +20,8 @@ import subprocess
 import sys
 import sysconfig
 
+from . import binding
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -27,6 +30,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd.so")
 PYCALL_SRC = os.path.join(CSRC, "pycall.cpp")
 PYCALL = os.path.join(PKG, "_pycall.so")
+PYCALL_STAMP = os.path.join(BUILD, "pycall.built_for")   # what the built one is for
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -52,11 +56,23 @@ def up_to_date() -> bool:
     return _fresh(LIB, _deps())
 
 
+def _pycall_fresh() -> bool:
+    if not _fresh(PYCALL, [PYCALL_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.join(INCLUDE, "ssd_diag.h"), os.path.abspath(__file__)]):
+        return False
+    try:
+        with open(PYCALL_STAMP) as f:
+            return f.read() == binding.pycall_target()
+    except OSError:
+        return False
+
+
 def _build_pycall(verbose: bool) -> None:
+    os.makedirs(BUILD, exist_ok=True)
+    target = binding.pycall_target()
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = PYCALL + f".tmp{os.getpid()}"
-    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+    cmd = [CXX, "-O2", "-std=c++17", f'-DSSD_BUILT_FOR="{target}"', "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"), PYCALL_SRC, "-o", tmp,
            "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
            "-Wl,-rpath,$ORIGIN"]
@@ -66,6 +82,8 @@ def _build_pycall(verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed on {PYCALL_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PYCALL)
+    with open(PYCALL_STAMP, "w") as f:
+        f.write(target)
 
 
 def _compile(src: str, verbose: bool, extra) -> str:
@@ -84,7 +102,7 @@ def _compile(src: str, verbose: bool, extra) -> str:
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if force or not up_to_date():
         _build_lib(verbose, ptxas_info)
-    if force or not _fresh(PYCALL, [PYCALL_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.join(INCLUDE, "ssd_diag.h"), os.path.abspath(__file__)]):
+    if force or not _pycall_fresh():
         _build_pycall(verbose)
     return LIB
 

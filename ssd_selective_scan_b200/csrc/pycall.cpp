@@ -9,6 +9,7 @@
 // argument is converted by its C type.
 //
 // No state; errors are Python exceptions (torch's own C++ ones are translated).
+// SSD_BUILT_FOR names the torch and Python of the headers (build.py).
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -383,4 +384,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycall", "Tensor checks and direc
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__pycall() { return PyModule_Create(&module); }
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__pycall()
+{
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", SSD_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}
