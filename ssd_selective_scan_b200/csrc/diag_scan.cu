@@ -574,9 +574,8 @@ template <typename T, bool PACKED, Mode MODE>
 cudaError_t launch_t(const DiagArgs& args, int seg, cudaStream_t s)
 {
     DiagArgs a = args;
-    constexpr uintptr_t four = 4 * sizeof(T);
     a.longest_first = PACKED && a.nseq > 1 && a.nseq <= kSortSeqs && a.rows / a.nseq >= kSortRows;
-    a.bc_aligned = a.bcs % 4 == 0 && reinterpret_cast<uintptr_t>(a.B) % four == 0 && reinterpret_cast<uintptr_t>(a.C) % four == 0;
+    a.bc_aligned = bc_aligned(a, sizeof(T));
     switch (tile_lanes(a.N)) {
         case 2: return launch_lpc<T, 2, PACKED, MODE>(a, seg, s);
         case 4: return launch_lpc<T, 4, PACKED, MODE>(a, seg, s);
