@@ -29,6 +29,8 @@
  *   - B, C have the element type `dtype`, token t, group g, n at
  *     B[t*bc_stride + g*N + n]; any element-aligned pointer and any stride of
  *     at least G*N (they are usually columns of a projection's rows).
+ *   - NaN in a row spoils what the formulas say and nothing else.  An
+ *     infinite u, B or dt_raw may give NaN where they give an infinity.
  *   - A [E][N], D [E], dt_bias [E], conv weights (16-byte aligned, as A) and
  *     states are float32;
  *     sums, states and gradients accumulate in float32.  A is expected <= 0
@@ -54,7 +56,8 @@
  * The packed calls start sequence r from slot init_slot[r] (from zero where
  * that is -1) and write a state at every row that is the last of its block
  * or of its sequence, to the slot of its block.  Rows behind cu[nseq] are
- * neither read nor written (outputs there stay as they were); slots that no
+ * not written (outputs there stay as they were) and no result depends on what
+ * they hold; slots that no
  * row's block ends in stay as they were.  Maps that ssd_state_map made
  * without an error are sound.  For any other map, each call checks on the
  * device what memory safety needs (ranges of rows, sequences and slots),
@@ -203,8 +206,9 @@ SSD_API ssd_status_t ssd_diag_scan_fwd_varlen(const void* u, int64_t u_stride, c
  *   dB, dC [b][L][G][N] dtype, written (summed over each group's channels)
  *   dA [E][N], dD, ddt_bias [E] float32, written (summed over the batch)
  *   dinit  [b][E][N] float32, written, may be NULL (not wanted)
- *   workspace  ssd_diag_scan_bwd_workspace_bytes(...) bytes: states every 4
- *          tokens and partial sums, no initial contents
+ *   workspace  ssd_diag_scan_bwd_workspace_bytes(...) bytes, no initial
+ *          contents: a float32 state every 4 tokens (b*L*E*N bytes: 671 MB for
+ *          8 x 2048 tokens of 2560 channels, N = 16) and partial sums
  * Deterministic: no atomics.  b == 0 or L == 0 zeroes dA, dD and ddt_bias
  * and copies dfinal (or zeros) into dinit.
  */

@@ -12,10 +12,12 @@
 // summed in registers over the tile, written per tile, and summed over tiles
 // by a second kernel in a fixed order: no atomics.
 //
-// Bound by instruction issue, close to HBM: 17 FMAs and 2 special functions
-// per element.  8 x 2048 rows of 4608 bf16 channels take 104 us with the sum
-// over tiles, 66% of the measured copy rate; 114 us with 128-row tiles, 125
-// with 512, 119 with groups of 2 rows, 139 with 2 channels a thread.
+// Bound by latency: 8 x 2048 rows of 4608 bf16 channels are 576 CTAs, 14 warps
+// an SM of the 16 that 128 registers allow, whose loads are what they wait for
+// most (35% of a warp's time; issue is 44% busy, DRAM 50%, FMA 44%, special
+// functions 37%).  104 us with the sum over tiles, 66% of the measured copy
+// rate; 114 us with 128-row tiles, 125 with 512, 119 with groups of 2 rows, 139
+// with 2 channels a thread.
 #include "conv4.cuh"
 #include "diag.h"
 

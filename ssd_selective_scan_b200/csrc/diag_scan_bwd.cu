@@ -545,14 +545,19 @@ __global__ void __launch_bounds__(kSumThreads) diag_sum_kernel(const SumArgs a)
 // with them, at 8 x 2048 rows of 2560 channels), this kernel gains from them
 // (1390 us whole, 2 or 3 CTAs on an SM for all of its time), so rows are cut
 // where whole sequences make less than kLeastPerSm CTAs an SM.  An SM holds
-// kPerSm at a time; the pieces are the longest that take the device up 2.5
-// times or more, else the shortest, and where those take it up less than 1.25
-// times, such as fit it at once (a few CTAs of a second round would take as long
-// as the first).  The whole call, 8 x 2048 x 2560: 512 rows (2.9 times) 1441 us,
-// 192 1452, 320 1473, 96 1517, 64 1576; 4 x 2048 x 2560: 384 rows 898, 256 940,
-// 160 962, 512 (1.4 times) 1000; 8 x 256 x 2048: 64 rows (2.3 times) 185, 96 210; 1 x
+// kPerSm at a time; the pieces are the longest of 512, 256, 128 and 64 rows that
+// take the device up 2.5 times or more, else 64, and where those take it up less
+// than 1.25 times, such as fit it at once (a few CTAs of a second round would
+// take as long as the first).  The whole call, 8 x 2048 x 2560: 512 rows (2.9
+// times) 1441 us, 192 1452, 320 1473, 96 1517, 64 1576; 4 x 2048 x 2560: 256
+// rows 940, 160 962, 512 (1.4 times) 1000, and 384 (1.9 times), which the rule
+// does not try, 898; 8 x 256 x 2048: 64 rows (2.3 times) 185, 96 210; 1 x
 // 2048 x 1024: 64 rows (1.15 times) 141, 96 120, 192 162; 2 x 517 x 784: 64
 // rows (0.95 times) 89, 96 112.
+// No piece is longer than 512 rows, and each folds G over all behind it: from
+// some 100000 rows a sequence on, that reading (E N 4 bytes a piece) grows with
+// the square of the rows: 8.6 GB at 1 x 262144 x 1024, N = 16, twice what the
+// kept states are.
 constexpr int kLeastPerSm = 12;
 constexpr int kPerSm = 3;
 constexpr int kPieceMost = 512, kPieceLeast = 64;

@@ -12,8 +12,10 @@
 // read once for the rows.  y's sums over a channel's lanes are exchanged for
 // all rows at once, each lane ending with some of the rows.
 //
-// 256 rows of 8192 bf16 channels, 16 states: 56 us, 5.1 TB/s, 77% of the
-// measured copy rate (8 rows a CTA, 7 CTAs an SM: 60 us; 16 rows: 73).
+// 256 rows of 8192 bf16 channels, 16 states, by slots: 55.8 us in a graph over
+// several pools, 5.1 TB/s, 78% of the measured copy rate; 58 as single calls,
+// 51 on one pool, part of which stays in L2.  (8 rows a CTA, 7 CTAs an SM: 60
+// us; 16 rows: 73.)
 #include "diag.cuh"
 #include "diag.h"
 

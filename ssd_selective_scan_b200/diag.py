@@ -16,7 +16,13 @@ A serving step with these calls::
 
 (``diag_state_update`` in the last line's place where every request brings one
 token); ``status`` is read by the caller after synchronising, and 0 means that
-every check on the device passed.
+every check on the device passed.  The calls do not wait for the device, so
+nothing else tells: without a ``status`` (or with one that is not read) a batch
+that a check refuses looks like an empty one, its outputs not written.
+
+With ``stream``, results are the caller's to use on either stream.  Inputs, and
+an ``out``, ``y`` or ``workspace`` that was given, have to be ready on that
+stream, and to live until its work on them is done (``Tensor.record_stream``).
 """
 from __future__ import annotations
 

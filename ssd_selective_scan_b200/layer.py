@@ -4,7 +4,8 @@ PyTorch is plumbing here: it allocates device memory and supplies the current
 CUDA stream.  Each function checks tensor shapes, allocates the outputs,
 passes raw pointers to the C entry point of the same name (``libssd``) and
 raises ``SsdError`` on any non-OK status.  All arithmetic runs in the CUDA
-kernels of libssd.so.
+kernels of libssd.so.  With ``stream``, every tensor of the call has to be ready
+on that stream and to live until its work is done (``Tensor.record_stream``).
 """
 from __future__ import annotations
 
